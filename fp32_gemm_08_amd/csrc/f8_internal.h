@@ -1,0 +1,82 @@
+// Internal declarations of the 8-bit block-scaled family: products,
+// quantisation and the root-mean-square norm.
+#pragma once
+
+#include "sgemm_f8.h"
+#include "sgemm_internal.h"
+
+namespace sgemm {
+
+constexpr int F8_BLOCK = 128;            // values per scale
+constexpr float F8_FLOOR = 0x1p-90f;     // least block maximum: scales stay normal numbers
+
+enum F8KernelId : int {
+    KID_F8_NONE = 0,
+    KID_F8_SKINNY = 80,   // up to 64 rows of A: 16 columns of C per workgroup, k split over its wavefronts
+    KID_F8_S = 81,        // 64 x 64 tile
+    KID_F8_M = 82,        // 128 x 128 tile
+    KID_F8_L = 83,        // 256 x 256 tile
+};
+
+struct F8GemmArgs {
+    const uint8_t *A, *B;
+    const float *SA, *SB;
+    void *C;
+    float *ws;                            // partial sums [split][M][N]; NULL: unsplit
+    int64_t lda, ldb, ldsa, ldsb, ldc;
+    int M, N, K;
+    int tiles_m, tiles_n;                 // output tiles
+    int kb_split;                         // k-blocks per split
+    float alpha, beta;
+    int c_type;
+    int vec_c;                            // C allows 4-element accesses
+};
+
+struct F8GemmPlan {
+    int kid = KID_F8_NONE;
+    int64_t tiles_m = 0, tiles_n = 0, splits = 1, bytes = 0;
+};
+F8GemmPlan f8_gemm_plan(bool row_b, int64_t M, int64_t N, int64_t K, bool aligned);
+hipError_t launch_f8_gemm(F8GemmArgs a, const F8GemmPlan &p, int format_a, int format_b, bool row_b, bool aligned,
+                          hipStream_t s);
+// C <- beta * C for a rows x cols C of any type.
+hipError_t launch_f8_scale(void *C, int64_t ldc, int rows, int cols, int c_type, float beta, hipStream_t s);
+
+struct F8QuantArgs {
+    const void *X;
+    uint8_t *Q, *QT;
+    float *S, *ST;
+    int64_t ldx, ldq, lds, ldqt, ldst;
+    int rows, cols;
+    int tiles_c;            // tiles along the columns
+    int vec_x, vec_q, vec_qt;
+};
+hipError_t launch_f8_quantize(F8QuantArgs a, bool tile, int format, int x_type, hipStream_t s);
+
+struct NormArgs {
+    const void *X, *R, *W;
+    void *H, *Y;
+    uint8_t *Q;
+    float *S, *rstd;
+    int64_t ldx, ldr, ldh, ldy, ldq, lds;
+    int rows, cols;
+    float eps;
+    int w_f32;              // W is FP32 (else of the rows' type)
+    int vec;                // every row of X, R, H, Y (and W) allows 16-byte accesses
+    int vec_q;              // every row of Q allows 8-byte stores
+};
+hipError_t launch_rmsnorm(const NormArgs &a, int type, hipStream_t s);
+
+struct NormBwdArgs {
+    const void *DY, *H, *W, *DH;
+    const float *rstd;
+    void *DX;
+    float *DW, *ws;         // ws: [groups][cols] partial sums of DW
+    int64_t lddy, ldh, lddh, lddx;
+    int rows, cols, groups;
+    int w_f32, vec;
+};
+int64_t rmsnorm_bwd_groups(int64_t rows, int64_t cols);
+hipError_t launch_rmsnorm_bwd(const NormBwdArgs &a, int type, hipStream_t s);
+
+}  // namespace sgemm

@@ -1,0 +1,158 @@
+// Device helpers of the 8-bit block-scaled family: element types, 8-bit
+// rounding and the block maximum.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include "f8_internal.h"
+
+namespace sgemm {
+
+typedef float f8_f32x4 __attribute__((ext_vector_type(4)));
+typedef int f8_i32x4 __attribute__((ext_vector_type(4)));
+typedef int f8_i32x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t f8_u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t f8_u32x4 __attribute__((ext_vector_type(4)));
+
+// Formats: 0 = e4m3, 1 = e5m2 (the matrix instruction's own numbering).
+template <int FMT> __device__ __forceinline__ constexpr float f8_largest() { return FMT == 0 ? 448.0f : 57344.0f; }
+
+// Four values rounded to 8 bits (to nearest, ties to even), value i in byte i.
+// The values are within the format's range by construction (or NaN).
+template <int FMT>
+__device__ __forceinline__ uint32_t f8_pack4(float a, float b, float c, float d)
+{
+    if constexpr (FMT == 0) {
+        const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+        return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, lo, true);
+    } else {
+        const int lo = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, 0, false);
+        return (uint32_t)__builtin_amdgcn_cvt_pk_bf8_f32(c, d, lo, true);
+    }
+}
+
+// Row elements: loads and stores of 8 consecutive ones as FP32.
+template <typename T> struct Elt;
+template <> struct Elt<float> {
+    static __device__ __forceinline__ void load8(const float *p, float (&v)[8])
+    {
+        const f8_f32x4 a = *reinterpret_cast<const f8_f32x4 *>(p), b = *reinterpret_cast<const f8_f32x4 *>(p + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = a[i];
+            v[4 + i] = b[i];
+        }
+    }
+    static __device__ __forceinline__ void store8(float *p, const float (&v)[8])
+    {
+        *reinterpret_cast<f8_f32x4 *>(p) = f8_f32x4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<f8_f32x4 *>(p + 4) = f8_f32x4{v[4], v[5], v[6], v[7]};
+    }
+    static __device__ __forceinline__ float get(const float *p) { return *p; }
+    static __device__ __forceinline__ void put(float *p, float v) { *p = v; }
+};
+template <typename T, typename V8> struct Elt16 {
+    static __device__ __forceinline__ void load8(const T *p, float (&v)[8])
+    {
+        const V8 a = *reinterpret_cast<const V8 *>(p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = (float)a[i];
+    }
+    static __device__ __forceinline__ void store8(T *p, const float (&v)[8])
+    {
+        V8 a;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            a[i] = (T)v[i];
+        *reinterpret_cast<V8 *>(p) = a;
+    }
+    static __device__ __forceinline__ float get(const T *p) { return (float)*p; }
+    static __device__ __forceinline__ void put(T *p, float v) { *p = (T)v; }
+};
+typedef _Float16 f8_h8 __attribute__((ext_vector_type(8)));
+typedef __bf16 f8_b8 __attribute__((ext_vector_type(8)));
+template <> struct Elt<_Float16> : Elt16<_Float16, f8_h8> {};
+template <> struct Elt<__bf16> : Elt16<__bf16, f8_b8> {};
+
+// Elements c .. c+7 of a row of `cols`, zero past its end.
+template <typename T>
+__device__ __forceinline__ void row_load8(const T *row, int c, int cols, bool vec, float (&v)[8])
+{
+    if (vec && c + 8 <= cols) {
+        Elt<T>::load8(row + c, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = c + i < cols ? Elt<T>::get(row + c + i) : 0.0f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void row_store8(T *row, int c, int cols, bool vec, const float (&v)[8])
+{
+    if (vec && c + 8 <= cols) {
+        Elt<T>::store8(row + c, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i < cols)
+                Elt<T>::put(row + c + i, v[i]);
+    }
+}
+// The same for 8 bytes held in two words.
+__device__ __forceinline__ void row_store8b(uint8_t *row, int c, int cols, bool vec, uint32_t lo, uint32_t hi)
+{
+    if (vec && c + 8 <= cols) {
+        *reinterpret_cast<f8_u32x2 *>(row + c) = f8_u32x2{lo, hi};
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i < cols)
+                row[c + i] = (uint8_t)((i < 4 ? lo >> (8 * i) : hi >> (8 * (i - 4))) & 0xff);
+    }
+}
+
+// |x| as an unsigned number: ordered as |x| is, infinity above every finite
+// value and NaN above infinity, so that an integer maximum carries a NaN
+// through (the FP32 maximum instruction drops it).
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+__device__ __forceinline__ uint32_t abs_max8(const float (&v)[8])
+{
+    uint32_t m = abs_bits(v[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i)
+        m = max(m, abs_bits(v[i]));
+    return m;
+}
+
+// Maximum over each aligned group of 16 lanes, in every lane of the group: a
+// butterfly of data-parallel primitives (swap pairs, swap pairs of two, mirror
+// the half row, mirror the row).
+__device__ __forceinline__ uint32_t max16(uint32_t m)
+{
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xf, 0xf, false));   // quad_perm 1,0,3,2
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xf, 0xf, false));   // quad_perm 2,3,0,1
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x141, 0xf, 0xf, false));  // row_half_mirror
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x140, 0xf, 0xf, false));  // row_mirror
+    return m;
+}
+
+// Sum over the 64 lanes of a wavefront, in every lane.
+__device__ __forceinline__ float wave_sum(float v)
+{
+#pragma unroll
+    for (int off = 32; off; off >>= 1)
+        v += __shfl_xor(v, off);
+    return v;
+}
+
+// A block's maximum (as bits) -> the factor that quantises it and its scale.
+template <int FMT>
+__device__ __forceinline__ void block_scale(uint32_t bits, float &inv, float &scale)
+{
+    const float a = __uint_as_float(max(bits, __float_as_uint(F8_FLOOR)));
+    inv = f8_largest<FMT>() / a;
+    scale = a / f8_largest<FMT>();
+}
+
+}  // namespace sgemm

@@ -1,0 +1,343 @@
+// 8-bit block-scaled product C = alpha * A * B^T + beta * C on the matrix
+// cores, which add up one k-block of 128 products; the FP32 factor sA*sB of
+// that k-block scales the sum, and a second FP32 sum runs over the k-blocks:
+//
+//   C[m][n] = alpha * sum_b sA[b][m] * sB[b][n] * (sum_{k in b} qA[m][k] * qB[n][k])
+//
+// A 16-bit C is computed by v_mfma_f32_16x16x128_f8f6f4.  That instruction
+// adds products in groups of 8, each group aligned to its largest product with
+// 13 bits kept below it (measured: 2^16 + 8 keeps the 8, 2^16 + 7 loses the 7;
+// on normally distributed operands the sum of 128 is off by 1.5e-5 of its
+// size), far below a 16-bit C's half step of 2^-9 or 2^-12, at twice the rate
+// of the 16-bit instructions.  An FP32 C is meant to hold more than that (a
+// gradient that is accumulated over many calls): its 8-bit operands are turned
+// into bf16, which holds every e4m3 and e5m2 value, and go through
+// v_mfma_f32_16x16x32_bf16, whose sums are FP32 (1e-8 on the same operands).
+//
+// The instructions take rows of B as their first operand and rows of A as their
+// second, so that lane l holds C[m = l % 16][n = 4*(l/16) .. +3]: four
+// consecutive columns of one row, one store, and one factor where a k-block's
+// B scale is the same for 128 columns.  Lane l supplies 32 values of row
+// l % 16 of each operand, the 16-byte chunks l/16 and 4 + l/16 of its 128
+// (which 32 is free as long as both operands agree: the sum runs over all).
+#include "f8_types.h"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace sgemm {
+namespace {
+
+typedef __attribute__((address_space(3))) void f8_lds;
+
+// A lane's 32 values of one row: as they are (EXACT = false), or as bf16.
+template <int FMT, bool EXACT> struct Frag;
+template <int FMT> struct Frag<FMT, false> {
+    f8_i32x8 v;
+    __device__ __forceinline__ void set(f8_i32x4 lo, f8_i32x4 hi)
+    {
+        v = f8_i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    }
+};
+template <int FMT> struct Frag<FMT, true> {
+    f8_b8 v[4];
+    static __device__ __forceinline__ void eight(int a, int b, f8_b8 &o)
+    {
+        typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+        b2 p[4];
+        if constexpr (FMT == 0) {
+            p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((unsigned)a, 1.0f, false);
+            p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((unsigned)a, 1.0f, true);
+            p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((unsigned)b, 1.0f, false);
+            p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((unsigned)b, 1.0f, true);
+        } else {
+            p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((unsigned)a, 1.0f, false);
+            p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((unsigned)a, 1.0f, true);
+            p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((unsigned)b, 1.0f, false);
+            p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((unsigned)b, 1.0f, true);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o[2 * i] = p[i][0];
+            o[2 * i + 1] = p[i][1];
+        }
+    }
+    __device__ __forceinline__ void set(f8_i32x4 lo, f8_i32x4 hi)
+    {
+        eight(lo[0], lo[1], v[0]);
+        eight(lo[2], lo[3], v[1]);
+        eight(hi[0], hi[1], v[2]);
+        eight(hi[2], hi[3], v[3]);
+    }
+};
+
+// The 128 products of a 16 x 16 block's k-block.
+template <int FA, int FB>
+__device__ __forceinline__ f8_f32x4 f8_mma(const Frag<FB, false> &b, const Frag<FA, false> &a)
+{
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, f8_f32x4{}, FB, FA, 0, 0, 0, 0);
+}
+template <int FA, int FB>
+__device__ __forceinline__ f8_f32x4 f8_mma(const Frag<FB, true> &b, const Frag<FA, true> &a)
+{
+    f8_f32x4 t{};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.v[i], a.v[i], t, 0, 0, 0);
+    return t;
+}
+
+// 16 bytes of a row at any byte address, of which the first `valid` count (the
+// rest read as zero): whole aligned words, of which only those that hold a
+// counted byte are read, shifted into place.
+__device__ __forceinline__ f8_i32x4 load16_any(const uint8_t *p, int valid)
+{
+    f8_i32x4 v{};
+    if (valid <= 0)
+        return v;
+    const int sh = (int)(reinterpret_cast<uintptr_t>(p) & 3);
+    const uint32_t *q = reinterpret_cast<const uint32_t *>(p - sh);
+    uint32_t d[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+        d[i] = 4 * i < sh + valid ? q[i] : 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t x = __builtin_amdgcn_alignbyte(d[i + 1], d[i], sh);
+        const int keep = valid - 4 * i;  // bytes of this word that count
+        v[i] = (int)(keep >= 4 ? x : keep <= 0 ? 0u : x & (0xffffffffu >> (8 * (4 - keep))));
+    }
+    return v;
+}
+
+// The same at a 16-byte aligned address: one load, masked.
+__device__ __forceinline__ f8_i32x4 keep16(f8_i32x4 x, int valid)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int keep = valid - 4 * i;
+        x[i] = keep >= 4 ? x[i] : keep <= 0 ? 0 : (int)((uint32_t)x[i] & (0xffffffffu >> (8 * (4 - keep))));
+    }
+    return x;
+}
+__device__ __forceinline__ f8_i32x4 load16_aligned(const uint8_t *p, int valid)
+{
+    if (valid <= 0)
+        return f8_i32x4{};
+    return keep16(*reinterpret_cast<const f8_i32x4 *>(p), valid);
+}
+
+// Columns n .. n+3 of row m of C (or of a split's partial sums).
+template <typename T>
+__device__ __forceinline__ void put4(const F8GemmArgs &g, int m, int n, f8_f32x4 v)
+{
+    T *p = static_cast<T *>(g.C) + (int64_t)m * g.ldc + n;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] *= g.alpha;
+    typedef T V4 __attribute__((ext_vector_type(4)));
+    if (g.vec_c && n + 4 <= g.N) {
+        if (g.beta != 0.0f) {
+            const V4 old = *reinterpret_cast<const V4 *>(p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = fmaf(g.beta, (float)old[i], v[i]);
+        }
+        V4 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            o[i] = (T)v[i];
+        *reinterpret_cast<V4 *>(p) = o;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < g.N)
+                p[i] = (T)(g.beta != 0.0f ? fmaf(g.beta, (float)p[i], v[i]) : v[i]);
+    }
+}
+__device__ __forceinline__ void store_c(const F8GemmArgs &g, int m, int n, const f8_f32x4 &v)
+{
+    if (m >= g.M || n >= g.N)
+        return;
+    if (g.c_type == SGEMM_TYPE_F32)
+        put4<float>(g, m, n, v);
+    else if (g.c_type == SGEMM_TYPE_BF16)
+        put4<__bf16>(g, m, n, v);
+    else
+        put4<_Float16>(g, m, n, v);
+}
+
+// ------------------------------------------------------------- tiles
+
+// BM rows of A and BN rows of B per workgroup, WGM x WGN wavefronts.  A stage
+// is one k-block of 128 bytes of every row, two stages rotate.  In LDS a row's
+// eight 16-byte chunks are permuted by (r ^ (r >> 3)) & 7, so that one chunk
+// of 8 (or of 16, over 64 banks) consecutive rows falls on distinct banks.
+template <int BM_, int BN_, int WGM_, int WGN_>
+struct F8Geo {
+    static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_;
+    static constexpr int NW = WGM * WGN, NT = 64 * NW;
+    static constexpr int WM = BM / WGM, WN = BN / WGN, FM = WM / 16, FN = WN / 16;
+    static constexpr int ROWS = BM + BN;
+    static constexpr int LOADS = ROWS / 8 / NW;     // 1 KB blocks of 8 rows per wavefront per stage
+    static constexpr int SC = ROWS * 4;             // scales of a stage, bytes
+    static constexpr int STAGE = ROWS * 128 + SC;
+    static_assert(WM % 16 == 0 && WN % 16 == 0 && (128 % WN == 0 || WN % 128 == 0), "whole 16 x 16 blocks");
+    static_assert(LOADS * 8 * NW == ROWS, "every wavefront loads whole blocks");
+    static_assert(2 * STAGE <= 160 * 1024, "two stages in the LDS");
+};
+
+__device__ __forceinline__ int f8_swz(int r) { return (r ^ (r >> 3)) & 7; }
+
+// Workgroup -> output tile: one contiguous run of tiles per XCD, walked 8
+// tile-rows at a time.
+__device__ __forceinline__ void f8_map_tile(int bid, int nbm, int nbn, int &tm, int &tn)
+{
+    const int nb = nbm * nbn;
+    const int id = (nb % 8 == 0) ? (bid % 8) * (nb / 8) + bid / 8 : bid;
+    const int group = 8 * nbn;
+    const int g = id / group, first_m = g * 8;
+    const int gm = min(nbm - first_m, 8);
+    tm = first_m + (id % group) % gm;
+    tn = (id % group) / gm;
+}
+
+// Simple form: stage a k-block through registers, multiply it, repeat.
+template <class G, int FA, int FB, bool ROWB, bool ALIGNED, bool EXACT>
+__global__ __launch_bounds__(G::NT) void f8_tile_kernel(F8GemmArgs g)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[G::STAGE];
+    float *sc = reinterpret_cast<float *>(smem + G::ROWS * 128);
+    int tm, tn;
+    f8_map_tile(blockIdx.x, g.tiles_m, g.tiles_n, tm, tn);
+    const int m0 = tm * G::BM, n0 = tn * G::BN;
+    const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = w / G::WGN, wn = w % G::WGN;
+
+    f8_f32x4 acc[G::FM][G::FN];
+#pragma unroll
+    for (int i = 0; i < G::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < G::FN; ++j)
+            acc[i][j] = f8_f32x4{};
+
+    const int nkb = (int)(((int64_t)g.K + 127) / 128);
+    for (int kb = 0; kb < nkb; ++kb) {
+        poison_lds(smem, G::STAGE);
+        // rows 0 .. BM-1 of a stage are A's, the others B's; rows past the
+        // matrix repeat its last one (their results are not stored)
+        for (int e = threadIdx.x; e < G::ROWS * 8; e += G::NT) {
+            const int r = e >> 3, c = e & 7;
+            const int64_t k = (int64_t)kb * 128 + 16 * c;
+            const int valid = (int)min<int64_t>(g.K - k, 16);
+            const uint8_t *p = r < G::BM ? g.A + (int64_t)min(m0 + r, g.M - 1) * g.lda + k
+                                         : g.B + (int64_t)min(n0 + r - G::BM, g.N - 1) * g.ldb + k;
+            const f8_i32x4 x = ALIGNED ? load16_aligned(p, valid) : load16_any(p, valid);
+            *reinterpret_cast<f8_i32x4 *>(smem + r * 128 + 16 * (c ^ f8_swz(r))) = x;
+        }
+        for (int r = threadIdx.x; r < G::BM + (ROWB ? G::BN : 0); r += G::NT)
+            sc[r] = r < G::BM ? g.SA[kb * g.ldsa + min(m0 + r, g.M - 1)]
+                              : g.SB[kb * g.ldsb + min(n0 + r - G::BM, g.N - 1)];
+        __syncthreads();
+        const float sb = ROWB ? 0.0f : g.SB[(int64_t)(min(n0 + wn * G::WN, g.N - 1) / 128) * g.ldsb + kb];
+        Frag<FB, EXACT> fb[G::FN];
+#pragma unroll
+        for (int j = 0; j < G::FN; ++j) {
+            const int r = G::BM + wn * G::WN + 16 * j + l16;
+            fb[j].set(*reinterpret_cast<const f8_i32x4 *>(smem + r * 128 + 16 * (q ^ f8_swz(r))),
+                         *reinterpret_cast<const f8_i32x4 *>(smem + r * 128 + 16 * ((q + 4) ^ f8_swz(r))));
+        }
+#pragma unroll
+        for (int i = 0; i < G::FM; ++i) {
+            const int r = wm * G::WM + 16 * i + l16;
+            Frag<FA, EXACT> fa;
+            fa.set(*reinterpret_cast<const f8_i32x4 *>(smem + r * 128 + 16 * (q ^ f8_swz(r))),
+                   *reinterpret_cast<const f8_i32x4 *>(smem + r * 128 + 16 * ((q + 4) ^ f8_swz(r))));
+            const float sa = sc[r];
+#pragma unroll
+            for (int j = 0; j < G::FN; ++j) {
+                const f8_f32x4 t = f8_mma<FA, FB>(fb[j], fa);
+                if constexpr (ROWB) {
+                    const f8_f32x4 s = *reinterpret_cast<const f8_f32x4 *>(sc + G::BM + wn * G::WN + 16 * j + 4 * q);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        acc[i][j][x] = fmaf(t[x], sa * s[x], acc[i][j][x]);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        acc[i][j][x] = fmaf(t[x], sa * sb, acc[i][j][x]);
+                }
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < G::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < G::FN; ++j)
+            store_c(g, m0 + wm * G::WM + 16 * i + l16, n0 + wn * G::WN + 16 * j + 4 * q, acc[i][j]);
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void f8_scale_kernel(T *C, int64_t ldc, int cols, float beta)
+{
+    const int64_t row = blockIdx.x;
+    for (int64_t c = threadIdx.x; c < cols; c += 256)
+        C[row * ldc + c] = (T)(beta != 0.0f ? beta * (float)C[row * ldc + c] : 0.0f);
+}
+
+typedef F8Geo<64, 64, 2, 2> GS;
+
+// The variant of a kernel for a call's formats, B blocks, alignment and type
+// of C: f is called with the template arguments as integral constants.
+template <bool V> using Bool = std::integral_constant<bool, V>;
+template <int V> using Int = std::integral_constant<int, V>;
+template <class F> void on_bool(bool v, F f) { v ? f(Bool<true>{}) : f(Bool<false>{}); }
+template <class F> void on_format(int v, F f) { v == SGEMM_F8_E4M3 ? f(Int<0>{}) : f(Int<1>{}); }
+
+template <class G>
+void launch_tile(const F8GemmArgs &a, int fa, int fb, bool row_b, bool aligned, hipStream_t s)
+{
+    const dim3 grid((unsigned)(a.tiles_m * a.tiles_n)), block(G::NT);
+    on_format(fa, [&](auto FA) { on_format(fb, [&](auto FB) { on_bool(row_b, [&](auto ROWB) {
+        on_bool(aligned, [&](auto AL) { on_bool(a.c_type == SGEMM_TYPE_F32, [&](auto EX) {
+            f8_tile_kernel<G, FA(), FB(), ROWB(), AL(), EX()><<<grid, block, 0, s>>>(a);
+        }); }); }); }); });
+}
+
+}  // namespace
+
+F8GemmPlan f8_gemm_plan(bool row_b, int64_t M, int64_t N, int64_t K, bool aligned)
+{
+    (void)row_b;
+    (void)K;
+    (void)aligned;
+    F8GemmPlan p;
+    p.kid = KID_F8_S;
+    p.tiles_m = (M + GS::BM - 1) / GS::BM;
+    p.tiles_n = (N + GS::BN - 1) / GS::BN;
+    return p;
+}
+
+hipError_t launch_f8_gemm(F8GemmArgs a, const F8GemmPlan &p, int format_a, int format_b, bool row_b, bool aligned,
+                          hipStream_t s)
+{
+    a.tiles_m = (int)p.tiles_m;
+    a.tiles_n = (int)p.tiles_n;
+    launch_tile<GS>(a, format_a, format_b, row_b, aligned, s);
+    return hipGetLastError();
+}
+
+hipError_t launch_f8_scale(void *C, int64_t ldc, int rows, int cols, int c_type, float beta, hipStream_t s)
+{
+    if (c_type == SGEMM_TYPE_F32)
+        f8_scale_kernel<<<(unsigned)rows, 256, 0, s>>>(static_cast<float *>(C), ldc, cols, beta);
+    else if (c_type == SGEMM_TYPE_FP16)
+        f8_scale_kernel<<<(unsigned)rows, 256, 0, s>>>(static_cast<_Float16 *>(C), ldc, cols, beta);
+    else
+        f8_scale_kernel<<<(unsigned)rows, 256, 0, s>>>(static_cast<__bf16 *>(C), ldc, cols, beta);
+    return hipGetLastError();
+}
+
+}  // namespace sgemm

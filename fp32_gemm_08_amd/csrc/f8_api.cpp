@@ -11,6 +11,7 @@ using namespace sgemm;
 namespace {
 
 constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1025;
+constexpr int64_t kMaxFastLd = int64_t{1} << 24;
 constexpr int64_t kMaxWorkItems = (int64_t{1} << 32) - 1;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -145,7 +146,8 @@ int sgemm_f8_gemm(int format_a, int format_b, int b_block, int c_type, int64_t M
     const Operand outs[2] = {oc, ows}, ins[4] = {oa, ob, osa, osb};
     if (aliased(outs, ins, -1, 0))
         return SGEMM_ERR_ALIAS;
-    const bool aligned = oa.rows_on(16) && ob.rows_on(16);
+    // the fast kernels' offsets within a tile of 256 rows are 32 bits wide
+    const bool aligned = oa.rows_on(16) && ob.rows_on(16) && (M <= 1 || lda <= kMaxFastLd) && (N <= 1 || ldb <= kMaxFastLd);
     F8GemmPlan p = f8_gemm_plan(b_block == SGEMM_F8_ROW, M, N, K, aligned);
     if (p.tiles_m * p.tiles_n * p.splits * threads_of(p.kid) > kMaxWorkItems)
         return SGEMM_ERR_INVALID_VALUE;
@@ -173,7 +175,7 @@ int sgemm_f8_gemm(int format_a, int format_b, int b_block, int c_type, int64_t M
     a.alpha = alpha;
     a.beta = beta;
     a.c_type = c_type;
-    a.vec_c = oc.rows_on(4 * type_bytes(c_type));
+    a.vec_c = oc.rows_on(16);
     (void)hipGetLastError();
     return finish(launch_f8_gemm(a, p, format_a, format_b, b_block == SGEMM_F8_ROW, aligned,
                                  reinterpret_cast<hipStream_t>(stream)));

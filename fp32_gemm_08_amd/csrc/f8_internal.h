@@ -29,7 +29,7 @@ struct F8GemmArgs {
     int kb_split;                         // k-blocks per split
     float alpha, beta;
     int c_type;
-    int vec_c;                            // C allows 4-element accesses
+    int vec_c;                            // every row of C starts on a 16-byte boundary
 };
 
 struct F8GemmPlan {

@@ -127,44 +127,49 @@ __device__ __forceinline__ f8_i32x4 load16_aligned(const uint8_t *p, int valid)
     return keep16(*reinterpret_cast<const f8_i32x4 *>(p), valid);
 }
 
-// Columns n .. n+3 of row m of C (or of a split's partial sums).
+// Columns n .. n+7 of row m of C <- alpha * v + beta * C.
 template <typename T>
-__device__ __forceinline__ void put4(const F8GemmArgs &g, int m, int n, f8_f32x4 v)
+__device__ __forceinline__ void put8(const F8GemmArgs &g, int m, int n, const float *v)
 {
-    T *p = static_cast<T *>(g.C) + (int64_t)m * g.ldc + n;
+    T *row = static_cast<T *>(g.C) + (int64_t)m * g.ldc;
+    float o[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        v[i] *= g.alpha;
-    typedef T V4 __attribute__((ext_vector_type(4)));
-    if (g.vec_c && n + 4 <= g.N) {
-        if (g.beta != 0.0f) {
-            const V4 old = *reinterpret_cast<const V4 *>(p);
+    for (int i = 0; i < 8; ++i)
+        o[i] = g.alpha * v[i];
+    if (g.beta != 0.0f) {
+        float old[8];
+        row_load8(row, n, g.N, g.vec_c, old);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[i] = fmaf(g.beta, (float)old[i], v[i]);
-        }
-        V4 o;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            o[i] = (T)v[i];
-        *reinterpret_cast<V4 *>(p) = o;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (n + i < g.N)
-                p[i] = (T)(g.beta != 0.0f ? fmaf(g.beta, (float)p[i], v[i]) : v[i]);
+        for (int i = 0; i < 8; ++i)
+            o[i] = fmaf(g.beta, old[i], o[i]);
     }
+    row_store8(row, n, g.N, g.vec_c, o);
 }
-__device__ __forceinline__ void store_c(const F8GemmArgs &g, int m, int n, const f8_f32x4 &v)
+
+// A wavefront's 16 rows of WN columns of C, of which lane l holds row l % 16,
+// columns 16j + 4*(l/16) .. +3: through `buf` (16 x (WN + 4) floats of this
+// wavefront's own), so that WN/8 lanes write one row together.
+template <int FN>
+__device__ __forceinline__ void store_rows(const F8GemmArgs &g, float *buf, int m, int n, const f8_f32x4 (&acc)[FN])
 {
-    if (m >= g.M || n >= g.N)
-        return;
-    if (g.c_type == SGEMM_TYPE_F32)
-        put4<float>(g, m, n, v);
-    else if (g.c_type == SGEMM_TYPE_BF16)
-        put4<__bf16>(g, m, n, v);
-    else
-        put4<_Float16>(g, m, n, v);
+    constexpr int PITCH = 16 * FN + 4, LANES = 2 * FN;  // lanes of a row
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+        *reinterpret_cast<f8_f32x4 *>(buf + (lane & 15) * PITCH + 16 * j + 4 * (lane >> 4)) = acc[j];
+#pragma unroll 1
+    for (int e = lane; e < 16 * LANES; e += 64) {
+        const int r = e / LANES, c = 8 * (e % LANES);
+        if (m + r >= g.M || n + c >= g.N)
+            continue;
+        const float *v = buf + r * PITCH + c;
+        if (g.c_type == SGEMM_TYPE_F32)
+            put8<float>(g, m + r, n + c, v);
+        else if (g.c_type == SGEMM_TYPE_BF16)
+            put8<__bf16>(g, m + r, n + c, v);
+        else
+            put8<_Float16>(g, m + r, n + c, v);
+    }
 }
 
 // ------------------------------------------------------------- tiles
@@ -183,9 +188,13 @@ struct F8Geo {
     static constexpr int SC = ROWS * 4;             // scales of a stage, bytes
     static constexpr int STAGE = ROWS * 128 + SC;
     static_assert(WM % 16 == 0 && WN % 16 == 0 && (128 % WN == 0 || WN % 128 == 0), "whole 16 x 16 blocks");
+    static constexpr int OUT = 16 * (WN + 4);       // floats that a wavefront's 16 rows of C pass through
+    static_assert(NW * OUT * 4 <= STAGE, "they fit into a stage");
     static_assert(LOADS * 8 * NW == ROWS, "every wavefront loads whole blocks");
     static_assert(2 * STAGE <= 160 * 1024, "two stages in the LDS");
 };
+
+template <typename T> __device__ __forceinline__ T f8_pick(bool first, T a, T b) { return first ? a : b; }
 
 __device__ __forceinline__ int f8_swz(int r) { return (r ^ (r >> 3)) & 7; }
 
@@ -272,11 +281,190 @@ __global__ __launch_bounds__(G::NT) void f8_tile_kernel(F8GemmArgs g)
         }
         __syncthreads();
     }
+    __syncthreads();
+    float *buf = reinterpret_cast<float *>(smem) + w * G::OUT;
+#pragma unroll
+    for (int i = 0; i < G::FM; ++i)
+        store_rows<G::FN>(g, buf, m0 + wm * G::WM + 16 * i, n0 + wn * G::WN, acc[i]);
+}
+
+// Pipelined form, for operands whose rows start on 16-byte boundaries: S stages
+// rotate, filled by direct global -> LDS loads.
+template <class G, int S_, bool ROWB>
+struct F8Pipe {
+    static constexpr int S = S_;
+    static constexpr int SCALES = G::BM + (ROWB ? G::BN : 64);  // floats of a stage
+    static constexpr int NSC = SCALES / 64;                     // loads that fetch them
+    static constexpr int STAGE = G::ROWS * 128 + SCALES * 4;
+    static constexpr int LOADS = G::LOADS + 1;                  // per wavefront and stage
+    static_assert(NSC <= G::NW && SCALES % 64 == 0, "one scale load per wavefront fetches all");
+    static_assert(S * STAGE <= 160 * 1024 && (S - 2) * LOADS <= 63, "LDS size, vmcnt range");
+};
+
+// One direct global -> LDS load: 16 (or 4) bytes per lane, lane i landing at
+// byte 16 * i (or 4 * i).
+__device__ __forceinline__ void f8_load_lds16(const void *src, uint8_t *lds)
+{
+    __builtin_amdgcn_global_load_lds(src, (f8_lds *)lds, 16, 0, 0);
+}
+__device__ __forceinline__ void f8_load_lds4(const void *src, uint8_t *lds)
+{
+    __builtin_amdgcn_global_load_lds(src, (f8_lds *)lds, 4, 0, 0);
+}
+
+// Wait until at most N of this wavefront's direct loads are outstanding and
+// its LDS accesses are done, then meet the others (gfx9 encoding: vmcnt bits
+// 3:0 and 15:14, expcnt 6:4 left at 7, lgkmcnt 11:8 = 0).
+template <int N>
+__device__ __forceinline__ void f8_wait_barrier()
+{
+    static_assert(N >= 0 && N <= 63, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((N & 0xF) | (0x7 << 4) | ((N >> 4) << 14));
+    asm volatile("s_barrier" ::: "memory");
+}
+
+template <class G, int S, int FA, int FB, bool ROWB, bool EXACT>
+__global__ __launch_bounds__(G::NT) void f8_pipe_kernel(F8GemmArgs g)
+{
+    typedef F8Pipe<G, S, ROWB> P;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[S * P::STAGE];
+    int tm, tn;
+    f8_map_tile(blockIdx.x, g.tiles_m, g.tiles_n, tm, tn);
+    const int m0 = tm * G::BM, n0 = tn * G::BN;
+    const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = w / G::WGN, wn = w % G::WGN;
+
+    // This lane's bytes in each of its wavefront's 1 KB blocks: row 8b + lane/8,
+    // chunk (lane % 8) ^ swizzle of that row; rows past the matrix repeat its
+    // last one.  Offsets from the tile's first row fit 32 bits (the plan's
+    // condition on the leading dimensions).
+    const uint8_t *base_a = g.A + (int64_t)m0 * g.lda, *base_b = g.B + (int64_t)n0 * g.ldb;
+    uint32_t off[G::LOADS];
+#pragma unroll
+    for (int j = 0; j < G::LOADS; ++j) {
+        const int b = w * G::LOADS + j, r = 8 * b + lane / 8;
+        const int rr = b < G::BM / 8 ? min(r, g.M - 1 - m0) : min(r - G::BM, g.N - 1 - n0);
+        off[j] = (uint32_t)rr * (uint32_t)(b < G::BM / 8 ? g.lda : g.ldb) + 16 * ((lane & 7) ^ f8_swz(r));
+    }
+    // This lane's scale: those of A's rows in the order (row % 16, row / 16) of a
+    // wavefront's rows, so that a lane reads its own together; those of B's
+    // columns in order, or of each fourth column.
+    const int sblock = w % P::NSC, si = 64 * sblock + lane;
+    const float *sp;
+    int64_t sstep;
+    if (si < G::BM) {
+        const int r = si / G::WM * G::WM + 16 * (si % G::FM) + si % G::WM / G::FM;
+        sp = g.SA + min(m0 + r, g.M - 1);
+        sstep = g.ldsa;
+    } else if constexpr (ROWB) {
+        sp = g.SB + min(n0 + si - G::BM, g.N - 1);
+        sstep = g.ldsb;
+    } else {
+        sp = g.SB + (int64_t)(min(n0 + 4 * (si - G::BM), g.N - 1) / 128) * g.ldsb;
+        sstep = 1;
+    }
+
+    const int nk = (int)(((int64_t)g.K + 127) / 128);
+    const int nfull = g.K / 128;                    // stages fetched by direct loads
+    auto issue = [&](int kb) {
+        uint8_t *st = smem + (kb % S) * P::STAGE;
+        poison_lds(st, P::STAGE);
+        f8_load_lds4(sp + kb * sstep, st + G::ROWS * 128 + 256 * sblock);
+        if (kb < nfull) {
+#pragma unroll
+            for (int j = 0; j < G::LOADS; ++j) {
+                const int b = w * G::LOADS + j;
+                f8_load_lds16(f8_pick(b < G::BM / 8, base_a, base_b) + (int64_t)kb * 128 + off[j], st + b * 1024);
+            }
+        } else {
+            // the last values of every row, through registers: what lies past them is zero
+#pragma unroll 1
+            for (int j = 0; j < G::LOADS; ++j) {
+                const int b = w * G::LOADS + j, r = 8 * b + lane / 8, c = (lane & 7) ^ f8_swz(r);
+                const int rr = b < G::BM / 8 ? min(r, g.M - 1 - m0) : min(r - G::BM, g.N - 1 - n0);
+                const uint8_t *p = f8_pick(b < G::BM / 8, base_a, base_b) +
+                                   rr * f8_pick(b < G::BM / 8, g.lda, g.ldb) + (int64_t)kb * 128 + 16 * c;
+                *reinterpret_cast<f8_i32x4 *>(st + b * 1024 + 16 * lane) = load16_aligned(p, g.K - kb * 128 - 16 * c);
+            }
+        }
+    };
+
+    f8_f32x4 acc[G::FM][G::FN];
 #pragma unroll
     for (int i = 0; i < G::FM; ++i)
 #pragma unroll
         for (int j = 0; j < G::FN; ++j)
-            store_c(g, m0 + wm * G::WM + 16 * i + l16, n0 + wn * G::WN + 16 * j + 4 * q, acc[i][j]);
+            acc[i][j] = f8_f32x4{};
+
+#pragma unroll
+    for (int st = 0; st < S - 1; ++st)
+        if (st < nk)
+            issue(st);
+    for (int kb = 0; kb < nk; ++kb) {
+        // stage kb has landed (and stage kb-1 is read by all): stages up to kb+S-2
+        // may be in flight, if they are all there and direct loads
+        if (S > 2 && kb + S - 2 < nfull)
+            f8_wait_barrier<(S - 2) * P::LOADS>();
+        else
+            f8_wait_barrier<0>();
+        if (kb + S - 1 < nk)
+            issue(kb + S - 1);
+        const uint8_t *st = smem + (kb % S) * P::STAGE;
+        const float *sc = reinterpret_cast<const float *>(st + G::ROWS * 128);
+        auto chunk = [&](int r, int c) {
+            return *reinterpret_cast<const f8_i32x4 *>(st + r * 128 + 16 * (c ^ f8_swz(r)));
+        };
+        float sa[G::FM];
+#pragma unroll
+        for (int i = 0; i < G::FM; ++i)
+            sa[i] = sc[wm * G::WM + l16 * G::FM + i];
+        if constexpr (!ROWB) {
+            const float sb = sc[G::BM + wn * G::WN / 4];
+#pragma unroll
+            for (int i = 0; i < G::FM; ++i)
+                sa[i] *= sb;
+        }
+        f8_f32x4 sbv[ROWB ? G::FN : 1];
+        if constexpr (ROWB) {
+#pragma unroll
+            for (int j = 0; j < G::FN; ++j)
+                sbv[j] = *reinterpret_cast<const f8_f32x4 *>(sc + G::BM + wn * G::WN + 16 * j + 4 * q);
+        }
+        Frag<FB, EXACT> fb[G::FN];
+#pragma unroll
+        for (int j = 0; j < G::FN; ++j) {
+            const int r = G::BM + wn * G::WN + 16 * j + l16;
+            fb[j].set(chunk(r, q), chunk(r, q + 4));
+        }
+        // 16 x 16 block e = i * FN + j: its products while block e-2 is scaled and added
+        constexpr int NB = G::FM * G::FN, LAG = 2;
+        f8_f32x4 t[LAG + 1];
+        Frag<FA, EXACT> fa;
+#pragma unroll
+        for (int e = 0; e < NB + LAG; ++e) {
+            if (e < NB) {
+                const int i = e / G::FN, j = e % G::FN;
+                if (j == 0) {
+                    const int r = wm * G::WM + 16 * i + l16;
+                    fa.set(chunk(r, q), chunk(r, q + 4));
+                }
+                t[e % (LAG + 1)] = f8_mma<FA, FB>(fb[j], fa);
+            }
+            if (e >= LAG) {
+                const int i = (e - LAG) / G::FN, j = (e - LAG) % G::FN;
+                const f8_f32x4 &u = t[(e - LAG) % (LAG + 1)];
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    acc[i][j][x] = fmaf(u[x], ROWB ? sa[i] * sbv[ROWB ? j : 0][x] : sa[i], acc[i][j][x]);
+            }
+        }
+    }
+    __syncthreads();
+    float *buf = reinterpret_cast<float *>(smem) + w * G::OUT;
+#pragma unroll
+    for (int i = 0; i < G::FM; ++i)
+        store_rows<G::FN>(g, buf, m0 + wm * G::WM + 16 * i, n0 + wn * G::WN, acc[i]);
 }
 
 template <typename T>
@@ -288,6 +476,8 @@ __global__ __launch_bounds__(256) void f8_scale_kernel(T *C, int64_t ldc, int co
 }
 
 typedef F8Geo<64, 64, 2, 2> GS;
+typedef F8Geo<128, 128, 2, 2> GM;
+typedef F8Geo<256, 256, 2, 4> GL;
 
 // The variant of a kernel for a call's formats, B blocks, alignment and type
 // of C: f is called with the template arguments as integral constants.
@@ -306,17 +496,34 @@ void launch_tile(const F8GemmArgs &a, int fa, int fb, bool row_b, bool aligned, 
         }); }); }); }); });
 }
 
+template <class G, int S>
+void launch_pipe(const F8GemmArgs &a, int fa, int fb, bool row_b, hipStream_t s)
+{
+    const dim3 grid((unsigned)(a.tiles_m * a.tiles_n)), block(G::NT);
+    on_format(fa, [&](auto FA) { on_format(fb, [&](auto FB) { on_bool(row_b, [&](auto ROWB) {
+        on_bool(a.c_type == SGEMM_TYPE_F32, [&](auto EX) {
+            f8_pipe_kernel<G, S, FA(), FB(), ROWB(), EX()><<<grid, block, 0, s>>>(a);
+        }); }); }); });
+}
+
 }  // namespace
 
 F8GemmPlan f8_gemm_plan(bool row_b, int64_t M, int64_t N, int64_t K, bool aligned)
 {
     (void)row_b;
     (void)K;
-    (void)aligned;
     F8GemmPlan p;
+    int64_t bm = GS::BM, bn = GS::BN;
     p.kid = KID_F8_S;
-    p.tiles_m = (M + GS::BM - 1) / GS::BM;
-    p.tiles_n = (N + GS::BN - 1) / GS::BN;
+    if (aligned && M * N >= (int64_t)256 * 256 * 128) {
+        p.kid = KID_F8_L;
+        bm = GL::BM, bn = GL::BN;
+    } else if (aligned && M > 64 && N > 64) {
+        p.kid = KID_F8_M;
+        bm = GM::BM, bn = GM::BN;
+    }
+    p.tiles_m = (M + bm - 1) / bm;
+    p.tiles_n = (N + bn - 1) / bn;
     return p;
 }
 
@@ -325,7 +532,12 @@ hipError_t launch_f8_gemm(F8GemmArgs a, const F8GemmPlan &p, int format_a, int f
 {
     a.tiles_m = (int)p.tiles_m;
     a.tiles_n = (int)p.tiles_n;
-    launch_tile<GS>(a, format_a, format_b, row_b, aligned, s);
+    if (p.kid == KID_F8_L)
+        launch_pipe<GL, 2>(a, format_a, format_b, row_b, s);
+    else if (p.kid == KID_F8_M)
+        launch_pipe<GM, 4>(a, format_a, format_b, row_b, s);
+    else
+        launch_tile<GS>(a, format_a, format_b, row_b, aligned, s);
     return hipGetLastError();
 }
 

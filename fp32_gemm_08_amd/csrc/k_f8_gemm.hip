@@ -34,10 +34,7 @@ typedef __attribute__((address_space(3))) void f8_lds;
 template <int FMT, bool EXACT> struct Frag;
 template <int FMT> struct Frag<FMT, false> {
     f8_i32x8 v;
-    __device__ __forceinline__ void set(f8_i32x4 lo, f8_i32x4 hi)
-    {
-        v = f8_i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-    }
+    __device__ __forceinline__ void set(const f8_i32x8 &x) { v = x; }
 };
 template <int FMT> struct Frag<FMT, true> {
     f8_b8 v[4];
@@ -62,14 +59,19 @@ template <int FMT> struct Frag<FMT, true> {
             o[2 * i + 1] = p[i][1];
         }
     }
-    __device__ __forceinline__ void set(f8_i32x4 lo, f8_i32x4 hi)
+    __device__ __forceinline__ void set(const f8_i32x8 &x)
     {
-        eight(lo[0], lo[1], v[0]);
-        eight(lo[2], lo[3], v[1]);
-        eight(hi[0], hi[1], v[2]);
-        eight(hi[2], hi[3], v[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            eight(x[2 * i], x[2 * i + 1], v[i]);
     }
 };
+
+// A lane's two chunks of a row as one operand.
+__device__ __forceinline__ f8_i32x8 f8_join(f8_i32x4 lo, f8_i32x4 hi)
+{
+    return f8_i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+}
 
 // The 128 products of a 16 x 16 block's k-block.
 template <int FA, int FB>
@@ -175,9 +177,12 @@ __device__ __forceinline__ void store_rows(const F8GemmArgs &g, float *buf, int 
 // ------------------------------------------------------------- tiles
 
 // BM rows of A and BN rows of B per workgroup, WGM x WGN wavefronts.  A stage
-// is one k-block of 128 bytes of every row, two stages rotate.  In LDS a row's
-// eight 16-byte chunks are permuted by (r ^ (r >> 3)) & 7, so that one chunk
-// of 8 (or of 16, over 64 banks) consecutive rows falls on distinct banks.
+// is one k-block of 128 bytes of every row.  In LDS a row's eight 16-byte chunks
+// are permuted by (r >> 1) & 7.  A 16-byte read takes its lanes 16 at a time
+// over 64 banks, in the groups 0-3, 12-15, 20-27 / 4-11, 16-19, 28-31 (and the
+// same of the upper half): each holds 16 rows, some at chunk q and some at
+// q ^ 1, which this permutation spreads over all banks.  (With the lanes' natural
+// order in mind, (r ^ (r >> 3)) & 7, half of the LDS cycles were bank conflicts.)
 template <int BM_, int BN_, int WGM_, int WGN_>
 struct F8Geo {
     static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_;
@@ -196,7 +201,7 @@ struct F8Geo {
 
 template <typename T> __device__ __forceinline__ T f8_pick(bool first, T a, T b) { return first ? a : b; }
 
-__device__ __forceinline__ int f8_swz(int r) { return (r ^ (r >> 3)) & 7; }
+__device__ __forceinline__ int f8_swz(int r) { return (r >> 1) & 7; }
 
 // Workgroup -> output tile: one contiguous run of tiles per XCD, walked 8
 // tile-rows at a time.
@@ -254,15 +259,15 @@ __global__ __launch_bounds__(G::NT) void f8_tile_kernel(F8GemmArgs g)
 #pragma unroll
         for (int j = 0; j < G::FN; ++j) {
             const int r = G::BM + wn * G::WN + 16 * j + l16;
-            fb[j].set(*reinterpret_cast<const f8_i32x4 *>(smem + r * 128 + 16 * (q ^ f8_swz(r))),
-                         *reinterpret_cast<const f8_i32x4 *>(smem + r * 128 + 16 * ((q + 4) ^ f8_swz(r))));
+            fb[j].set(f8_join(*reinterpret_cast<const f8_i32x4 *>(smem + r * 128 + 16 * (q ^ f8_swz(r))),
+                              *reinterpret_cast<const f8_i32x4 *>(smem + r * 128 + 16 * ((q + 4) ^ f8_swz(r)))));
         }
 #pragma unroll
         for (int i = 0; i < G::FM; ++i) {
             const int r = wm * G::WM + 16 * i + l16;
             Frag<FA, EXACT> fa;
-            fa.set(*reinterpret_cast<const f8_i32x4 *>(smem + r * 128 + 16 * (q ^ f8_swz(r))),
-                   *reinterpret_cast<const f8_i32x4 *>(smem + r * 128 + 16 * ((q + 4) ^ f8_swz(r))));
+            fa.set(f8_join(*reinterpret_cast<const f8_i32x4 *>(smem + r * 128 + 16 * (q ^ f8_swz(r))),
+                           *reinterpret_cast<const f8_i32x4 *>(smem + r * 128 + 16 * ((q + 4) ^ f8_swz(r)))));
             const float sa = sc[r];
 #pragma unroll
             for (int j = 0; j < G::FN; ++j) {
@@ -301,11 +306,14 @@ struct F8Pipe {
     static_assert(S * STAGE <= 160 * 1024 && (S - 2) * LOADS <= 63, "LDS size, vmcnt range");
 };
 
-// One direct global -> LDS load: 16 (or 4) bytes per lane, lane i landing at
-// byte 16 * i (or 4 * i).
-__device__ __forceinline__ void f8_load_lds16(const void *src, uint8_t *lds)
+// One direct global -> LDS load of 16 bytes per lane from `base` + the lane's
+// offset (a buffer load: the base stays in scalar registers), lane i landing at
+// byte 16 * i; and one of 4 bytes per lane.
+__device__ __forceinline__ void f8_load_lds16(const uint8_t *base, uint32_t off, uint8_t *lds)
 {
-    __builtin_amdgcn_global_load_lds(src, (f8_lds *)lds, 16, 0, 0);
+    const __amdgpu_buffer_rsrc_t rsrc =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base), 0, 0xffffffff, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (f8_lds *)lds, 16, off, 0, 0, 0);
 }
 __device__ __forceinline__ void f8_load_lds4(const void *src, uint8_t *lds)
 {
@@ -375,7 +383,7 @@ __global__ __launch_bounds__(G::NT) void f8_pipe_kernel(F8GemmArgs g)
 #pragma unroll
             for (int j = 0; j < G::LOADS; ++j) {
                 const int b = w * G::LOADS + j;
-                f8_load_lds16(f8_pick(b < G::BM / 8, base_a, base_b) + (int64_t)kb * 128 + off[j], st + b * 1024);
+                f8_load_lds16(f8_pick(b < G::BM / 8, base_a, base_b) + (int64_t)kb * 128, off[j], st + b * 1024);
             }
         } else {
             // the last values of every row, through registers: what lies past them is zero
@@ -397,67 +405,102 @@ __global__ __launch_bounds__(G::NT) void f8_pipe_kernel(F8GemmArgs g)
         for (int j = 0; j < G::FN; ++j)
             acc[i][j] = f8_f32x4{};
 
+    // Where this lane's two chunks of row l16 of a block of 16 rows lie, and of
+    // row 16i + l16 of its wavefront's rows from `first` on.
+    const uint32_t lo = l16 * 128 + 16 * (q ^ f8_swz(l16)), hi = lo ^ 64;
+    const uint32_t at_a = wm * G::WM * 128, at_b = (G::BM + wn * G::WN) * 128;
+    auto read = [&](const uint8_t *st, uint32_t first, int i) {
+        return f8_join(*reinterpret_cast<const f8_i32x4 *>(st + first + lo + i * 2048),
+                       *reinterpret_cast<const f8_i32x4 *>(st + first + hi + i * 2048));
+    };
+
+    // Pipeline.  At the start of a step the fragments of the B rows and of the
+    // first A rows are in registers.  Each row of blocks reads the next A rows
+    // under its products.  Before the last row every wavefront has read all of
+    // this stage: there the wavefronts meet, the stage after the next S-1 is
+    // requested into its place, and the next stage's fragments are read under
+    // the last row's products.
 #pragma unroll
-    for (int st = 0; st < S - 1; ++st)
+    for (int st = 0; st < S; ++st)
         if (st < nk)
             issue(st);
+    if (S > 1 && S - 1 < nfull)
+        f8_wait_barrier<(S - 1) * P::LOADS>();
+    else
+        f8_wait_barrier<0>();
+    Frag<FB, EXACT> fb[G::FN];
+    f8_i32x8 ra[2];
+#pragma unroll
+    for (int j = 0; j < G::FN; ++j)
+        fb[j].set(read(smem, at_b, j));
+    ra[0] = read(smem, at_a, 0);
     for (int kb = 0; kb < nk; ++kb) {
-        // stage kb has landed (and stage kb-1 is read by all): stages up to kb+S-2
-        // may be in flight, if they are all there and direct loads
-        if (S > 2 && kb + S - 2 < nfull)
-            f8_wait_barrier<(S - 2) * P::LOADS>();
-        else
-            f8_wait_barrier<0>();
-        if (kb + S - 1 < nk)
-            issue(kb + S - 1);
-        const uint8_t *st = smem + (kb % S) * P::STAGE;
+        const uint8_t *st = smem + (kb % S) * P::STAGE, *next = smem + ((kb + 1) % S) * P::STAGE;
         const float *sc = reinterpret_cast<const float *>(st + G::ROWS * 128);
-        auto chunk = [&](int r, int c) {
-            return *reinterpret_cast<const f8_i32x4 *>(st + r * 128 + 16 * (c ^ f8_swz(r)));
-        };
-        float sa[G::FM];
-#pragma unroll
-        for (int i = 0; i < G::FM; ++i)
-            sa[i] = sc[wm * G::WM + l16 * G::FM + i];
-        if constexpr (!ROWB) {
-            const float sb = sc[G::BM + wn * G::WN / 4];
-#pragma unroll
-            for (int i = 0; i < G::FM; ++i)
-                sa[i] *= sb;
-        }
+        float sa[G::FM], sb = 1.0f;
         f8_f32x4 sbv[ROWB ? G::FN : 1];
-        if constexpr (ROWB) {
-#pragma unroll
-            for (int j = 0; j < G::FN; ++j)
-                sbv[j] = *reinterpret_cast<const f8_f32x4 *>(sc + G::BM + wn * G::WN + 16 * j + 4 * q);
-        }
-        Frag<FB, EXACT> fb[G::FN];
-#pragma unroll
-        for (int j = 0; j < G::FN; ++j) {
-            const int r = G::BM + wn * G::WN + 16 * j + l16;
-            fb[j].set(chunk(r, q), chunk(r, q + 4));
-        }
-        // 16 x 16 block e = i * FN + j: its products while block e-2 is scaled and added
-        constexpr int NB = G::FM * G::FN, LAG = 2;
+        // 16 x 16 block e = i * FN + j: its products while block e - LAG is scaled and
+        // added (the wait for a product is then covered by the work between).  What the
+        // next row needs is read right after a row's first product: the wait that comes
+        // before each row then finds reads that are a row old.
+        constexpr int NB = G::FM * G::FN, LAG = EXACT ? 2 : 3;
         f8_f32x4 t[LAG + 1];
         Frag<FA, EXACT> fa;
 #pragma unroll
         for (int e = 0; e < NB + LAG; ++e) {
+            const int i = e / G::FN, j = e % G::FN;
             if (e < NB) {
-                const int i = e / G::FN, j = e % G::FN;
-                if (j == 0) {
-                    const int r = wm * G::WM + 16 * i + l16;
-                    fa.set(chunk(r, q), chunk(r, q + 4));
-                }
+                if (j == 0)
+                    fa.set(ra[i & 1]);
                 t[e % (LAG + 1)] = f8_mma<FA, FB>(fb[j], fa);
+                __builtin_amdgcn_sched_barrier(0);
+                if (e == 0) {
+#pragma unroll
+                    for (int x = 0; x < G::FM; ++x)
+                        sa[x] = sc[wm * G::WM + l16 * G::FM + x];
+                    if constexpr (ROWB) {
+#pragma unroll
+                        for (int x = 0; x < G::FN; ++x)
+                            sbv[x] = *reinterpret_cast<const f8_f32x4 *>(sc + G::BM + wn * G::WN + 16 * x + 4 * q);
+                    } else {
+                        sb = sc[G::BM + wn * G::WN / 4];
+                    }
+                }
+                if (j == 0 && i + 1 < G::FM)
+                    ra[(i + 1) & 1] = read(st, at_a, i + 1);
+                if (j == 0 && i + 1 == G::FM) {
+                    // stage kb+1 has landed: stages up to kb+S-1 may be in flight, if they
+                    // are all there and direct loads
+                    if (S > 2 && kb + S - 1 < nfull)
+                        f8_wait_barrier<(S - 2) * P::LOADS>();
+                    else
+                        f8_wait_barrier<0>();
+                    if (kb + S < nk)
+                        issue(kb + S);
+                    ra[0] = read(next, at_a, 0);
+                }
+                if (!EXACT && i + 1 == G::FM)
+                    fb[j].set(read(next, at_b, j));
+                __builtin_amdgcn_sched_barrier(0);
             }
             if (e >= LAG) {
-                const int i = (e - LAG) / G::FN, j = (e - LAG) % G::FN;
+                const int pi = (e - LAG) / G::FN, pj = (e - LAG) % G::FN;
                 const f8_f32x4 &u = t[(e - LAG) % (LAG + 1)];
+                if (!ROWB && pj == 0)
+                    sa[pi] *= sb;
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                    acc[i][j][x] = fmaf(u[x], ROWB ? sa[i] * sbv[ROWB ? j : 0][x] : sa[i], acc[i][j][x]);
+                    acc[pi][pj][x] = fmaf(u[x], ROWB ? sa[pi] * sbv[ROWB ? pj : 0][x] : sa[pi], acc[pi][pj][x]);
+                // the additions stay here: the compiler would sink them below the
+                // branches of the last row, and keep all products in registers till then
+                asm volatile("" : "+v"(acc[pi][pj]));
             }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (EXACT) {
+#pragma unroll
+            for (int j = 0; j < G::FN; ++j)
+                fb[j].set(read(next, at_b, j));
         }
     }
     __syncthreads();

@@ -147,7 +147,8 @@ int sgemm_f8_gemm(int format_a, int format_b, int b_block, int c_type, int64_t M
     if (aliased(outs, ins, -1, 0))
         return SGEMM_ERR_ALIAS;
     // the fast kernels' offsets within a tile of 256 rows are 32 bits wide
-    const bool aligned = oa.rows_on(16) && ob.rows_on(16) && (M <= 1 || lda <= kMaxFastLd) && (N <= 1 || ldb <= kMaxFastLd);
+    const bool aligned = oa.rows_on(16) && ob.rows_on(16) && (M <= 1 || lda <= kMaxFastLd) && (N <= 1 || ldb <= kMaxFastLd) &&
+                         (b_block == SGEMM_F8_ROW || N <= 128 || ldsb <= kMaxFastLd);
     F8GemmPlan p = f8_gemm_plan(b_block == SGEMM_F8_ROW, M, N, K, aligned);
     if (p.tiles_m * p.tiles_n * p.splits * threads_of(p.kid) > kMaxWorkItems)
         return SGEMM_ERR_INVALID_VALUE;

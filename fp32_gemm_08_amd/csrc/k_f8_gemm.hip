@@ -303,22 +303,29 @@ struct F8Pipe {
     static constexpr int STAGE = G::ROWS * 128 + SCALES * 4;
     static constexpr int LOADS = G::LOADS + 1;                  // per wavefront and stage
     static_assert(NSC <= G::NW && SCALES % 64 == 0, "one scale load per wavefront fetches all");
+    static_assert(G::LOADS < (G::FM - 1) * G::FN, "a step's loads come before its last row");
     static_assert(S * STAGE <= 160 * 1024 && (S - 2) * LOADS <= 63, "LDS size, vmcnt range");
 };
 
-// One direct global -> LDS load of 16 bytes per lane from `base` + the lane's
-// offset (a buffer load: the base stays in scalar registers), lane i landing at
-// byte 16 * i; and one of 4 bytes per lane.
-__device__ __forceinline__ void f8_load_lds16(const uint8_t *base, uint32_t off, uint8_t *lds)
+// Direct global -> LDS loads of 16 (or 4) bytes per lane from `base` + the lane's
+// offset, lane i landing at byte 16 * i (or 4 * i).  They are buffer loads: the
+// base stays in scalar registers, and offsets from `bytes` on deliver zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t f8_rsrc(const void *base, uint32_t bytes)
 {
-    const __amdgpu_buffer_rsrc_t rsrc =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base), 0, 0xffffffff, 0x00020000);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (f8_lds *)lds, 16, off, 0, 0, 0);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, bytes, 0x00020000);
 }
-__device__ __forceinline__ void f8_load_lds4(const void *src, uint8_t *lds)
+__device__ __forceinline__ void f8_load_lds16(const void *base, uint32_t bytes, uint32_t off, uint8_t *lds)
 {
-    __builtin_amdgcn_global_load_lds(src, (f8_lds *)lds, 4, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(f8_rsrc(base, bytes), (f8_lds *)lds, 16, off, 0, 0, 0);
 }
+__device__ __forceinline__ void f8_load_lds4(const void *base, uint32_t bytes, uint32_t off, uint8_t *lds)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(f8_rsrc(base, bytes), (f8_lds *)lds, 4, off, 0, 0, 0);
+}
+// The range check takes each 4 bytes by their own offset against the count of
+// bytes, so the offset that is meant to be out of range starts at that count.
+constexpr uint32_t F8_ALL = 0xfffffff0u;
+constexpr uint32_t F8_PAST = F8_ALL;
 
 // Wait until at most N of this wavefront's direct loads are outstanding and
 // its LDS accesses are done, then meet the others (gfx9 encoding: vmcnt bits
@@ -345,7 +352,7 @@ __global__ __launch_bounds__(G::NT) void f8_pipe_kernel(F8GemmArgs g)
 
     // This lane's bytes in each of its wavefront's 1 KB blocks: row 8b + lane/8,
     // chunk (lane % 8) ^ swizzle of that row; rows past the matrix repeat its
-    // last one.  Offsets from the tile's first row fit 32 bits (the plan's
+    // last one.  Offsets from the tile's first row fit 32 bits (the caller's
     // condition on the leading dimensions).
     const uint8_t *base_a = g.A + (int64_t)m0 * g.lda, *base_b = g.B + (int64_t)n0 * g.ldb;
     uint32_t off[G::LOADS];
@@ -359,43 +366,47 @@ __global__ __launch_bounds__(G::NT) void f8_pipe_kernel(F8GemmArgs g)
     // wavefront's rows, so that a lane reads its own together; those of B's
     // columns in order, or of each fourth column.
     const int sblock = w % P::NSC, si = 64 * sblock + lane;
-    const float *sp;
+    const bool scale_a = 64 * sblock < G::BM;
+    const float *sbase;
     int64_t sstep;
-    if (si < G::BM) {
-        const int r = si / G::WM * G::WM + 16 * (si % G::FM) + si % G::WM / G::FM;
-        sp = g.SA + min(m0 + r, g.M - 1);
+    uint32_t soff;
+    if (scale_a) {
+        sbase = g.SA + m0;
         sstep = g.ldsa;
+        soff = 4u * (uint32_t)min(si / G::WM * G::WM + 16 * (si % G::FM) + si % G::WM / G::FM, g.M - 1 - m0);
     } else if constexpr (ROWB) {
-        sp = g.SB + min(n0 + si - G::BM, g.N - 1);
+        sbase = g.SB + n0;
         sstep = g.ldsb;
+        soff = 4u * (uint32_t)min(si - G::BM, g.N - 1 - n0);
     } else {
-        sp = g.SB + (int64_t)(min(n0 + 4 * (si - G::BM), g.N - 1) / 128) * g.ldsb;
+        sbase = g.SB + (int64_t)(n0 / 128) * g.ldsb;
         sstep = 1;
+        soff = 4u * (uint32_t)(min(n0 + 4 * (si - G::BM), g.N - 1) / 128 - n0 / 128) * (uint32_t)g.ldsb;
     }
 
     const int nk = (int)(((int64_t)g.K + 127) / 128);
-    const int nfull = g.K / 128;                    // stages fetched by direct loads
-    auto issue = [&](int kb) {
+    const int tail = g.K - (nk - 1) * 128;          // values of the last stage's rows
+    // Load j of stage kb (j = LOADS: its scales).  Chunks past K deliver zeros, and
+    // so do stages past the last, so that every step makes the same loads.
+    auto fetch = [&](int kb, int j) {
         uint8_t *st = smem + (kb % S) * P::STAGE;
-        poison_lds(st, P::STAGE);
-        f8_load_lds4(sp + kb * sstep, st + G::ROWS * 128 + 256 * sblock);
-        if (kb < nfull) {
-#pragma unroll
-            for (int j = 0; j < G::LOADS; ++j) {
-                const int b = w * G::LOADS + j;
-                f8_load_lds16(f8_pick(b < G::BM / 8, base_a, base_b) + (int64_t)kb * 128, off[j], st + b * 1024);
-            }
-        } else {
-            // the last values of every row, through registers: what lies past them is zero
-#pragma unroll 1
-            for (int j = 0; j < G::LOADS; ++j) {
-                const int b = w * G::LOADS + j, r = 8 * b + lane / 8, c = (lane & 7) ^ f8_swz(r);
-                const int rr = b < G::BM / 8 ? min(r, g.M - 1 - m0) : min(r - G::BM, g.N - 1 - n0);
-                const uint8_t *p = f8_pick(b < G::BM / 8, base_a, base_b) +
-                                   rr * f8_pick(b < G::BM / 8, g.lda, g.ldb) + (int64_t)kb * 128 + 16 * c;
-                *reinterpret_cast<f8_i32x4 *>(st + b * 1024 + 16 * lane) = load16_aligned(p, g.K - kb * 128 - 16 * c);
-            }
+        const uint32_t bytes = kb < nk ? F8_ALL : 0;
+        if (j == G::LOADS) {
+            f8_load_lds4(sbase + kb * sstep, bytes, soff, st + G::ROWS * 128 + 256 * sblock);
+            return;
         }
+        const int b = w * G::LOADS + j, c = (lane & 7) ^ f8_swz(8 * b + lane / 8);
+        const uint32_t o = kb == nk - 1 && 16 * c >= tail ? F8_PAST : off[j];
+        f8_load_lds16(f8_pick(b < G::BM / 8, base_a, base_b) + (int64_t)kb * 128, bytes, o, st + b * 1024);
+    };
+    // The bytes past K of the chunk that holds the last values: zeros.
+    auto mask_tail = [&](int kb) {
+        for (int r = threadIdx.x; r < G::ROWS; r += G::NT) {
+            f8_i32x4 *p = reinterpret_cast<f8_i32x4 *>(smem + (kb % S) * P::STAGE + r * 128 +
+                                                       16 * ((tail / 16) ^ f8_swz(r)));
+            *p = keep16(*p, tail % 16);
+        }
+        __syncthreads();
     };
 
     f8_f32x4 acc[G::FM][G::FN];
@@ -416,18 +427,19 @@ __global__ __launch_bounds__(G::NT) void f8_pipe_kernel(F8GemmArgs g)
 
     // Pipeline.  At the start of a step the fragments of the B rows and of the
     // first A rows are in registers.  Each row of blocks reads the next A rows
-    // under its products.  Before the last row every wavefront has read all of
-    // this stage: there the wavefronts meet, the stage after the next S-1 is
-    // requested into its place, and the next stage's fragments are read under
-    // the last row's products.
+    // under its products.  The stage S-1 ahead is requested under the first rows,
+    // into the place of the stage before this one.  In the last row every
+    // wavefront has read all of this stage: there the wavefronts meet, and the
+    // next stage's fragments are read under the last row's products.
+    for (int st = 0; st < S - 1; ++st) {
+        poison_lds(smem + st * P::STAGE, P::STAGE);
 #pragma unroll
-    for (int st = 0; st < S; ++st)
-        if (st < nk)
-            issue(st);
-    if (S > 1 && S - 1 < nfull)
-        f8_wait_barrier<(S - 1) * P::LOADS>();
-    else
-        f8_wait_barrier<0>();
+        for (int j = 0; j <= G::LOADS; ++j)
+            fetch(st, j);
+    }
+    f8_wait_barrier<(S - 2) * P::LOADS>();
+    if (nk == 1 && tail % 16)
+        mask_tail(0);
     Frag<FB, EXACT> fb[G::FN];
     f8_i32x8 ra[2];
 #pragma unroll
@@ -437,6 +449,7 @@ __global__ __launch_bounds__(G::NT) void f8_pipe_kernel(F8GemmArgs g)
     for (int kb = 0; kb < nk; ++kb) {
         const uint8_t *st = smem + (kb % S) * P::STAGE, *next = smem + ((kb + 1) % S) * P::STAGE;
         const float *sc = reinterpret_cast<const float *>(st + G::ROWS * 128);
+        poison_lds(smem + ((kb + S - 1) % S) * P::STAGE, P::STAGE);
         float sa[G::FM], sb = 1.0f;
         f8_f32x4 sbv[ROWB ? G::FN : 1];
         // 16 x 16 block e = i * FN + j: its products while block e - LAG is scaled and
@@ -468,15 +481,12 @@ __global__ __launch_bounds__(G::NT) void f8_pipe_kernel(F8GemmArgs g)
                 }
                 if (j == 0 && i + 1 < G::FM)
                     ra[(i + 1) & 1] = read(st, at_a, i + 1);
+                if (e <= G::LOADS)
+                    fetch(kb + S - 1, e);
                 if (j == 0 && i + 1 == G::FM) {
-                    // stage kb+1 has landed: stages up to kb+S-1 may be in flight, if they
-                    // are all there and direct loads
-                    if (S > 2 && kb + S - 1 < nfull)
-                        f8_wait_barrier<(S - 2) * P::LOADS>();
-                    else
-                        f8_wait_barrier<0>();
-                    if (kb + S < nk)
-                        issue(kb + S);
+                    f8_wait_barrier<(S - 2) * P::LOADS>();  // stage kb+1 has landed
+                    if (kb + 2 == nk && tail % 16)
+                        mask_tail(kb + 1);
                     ra[0] = read(next, at_a, 0);
                 }
                 if (!EXACT && i + 1 == G::FM)
@@ -492,7 +502,7 @@ __global__ __launch_bounds__(G::NT) void f8_pipe_kernel(F8GemmArgs g)
                 for (int x = 0; x < 4; ++x)
                     acc[pi][pj][x] = fmaf(u[x], ROWB ? sa[pi] * sbv[ROWB ? pj : 0][x] : sa[pi], acc[pi][pj][x]);
                 // the additions stay here: the compiler would sink them below the
-                // branches of the last row, and keep all products in registers till then
+                // branch of the last row, and keep all products in registers till then
                 asm volatile("" : "+v"(acc[pi][pj]));
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -503,7 +513,8 @@ __global__ __launch_bounds__(G::NT) void f8_pipe_kernel(F8GemmArgs g)
                 fb[j].set(read(next, at_b, j));
         }
     }
-    __syncthreads();
+    // the stages requested past the last one land before the LDS is used again
+    f8_wait_barrier<0>();
     float *buf = reinterpret_cast<float *>(smem) + w * G::OUT;
 #pragma unroll
     for (int i = 0; i < G::FM; ++i)

@@ -39,6 +39,9 @@ struct F8GemmPlan {
 F8GemmPlan f8_gemm_plan(bool row_b, int64_t M, int64_t N, int64_t K, bool aligned);
 hipError_t launch_f8_gemm(F8GemmArgs a, const F8GemmPlan &p, int format_a, int format_b, bool row_b, bool aligned,
                           hipStream_t s);
+// M <= 64, aligned operands: columns per workgroup, and the launch.
+int f8_skinny_cols(bool row_b, int64_t N);
+hipError_t launch_f8_skinny(const F8GemmArgs &a, int format_a, int format_b, bool row_b, hipStream_t s);
 // C <- beta * C for a rows x cols C of any type.
 hipError_t launch_f8_scale(void *C, int64_t ldc, int rows, int cols, int c_type, float beta, hipStream_t s);
 

@@ -176,7 +176,6 @@ int sgemm_f8_gemm(int format_a, int format_b, int b_block, int c_type, int64_t M
     a.alpha = alpha;
     a.beta = beta;
     a.c_type = c_type;
-    a.vec_c = oc.rows_on(16);
     (void)hipGetLastError();
     return finish(launch_f8_gemm(a, p, format_a, format_b, b_block == SGEMM_F8_ROW, aligned,
                                  reinterpret_cast<hipStream_t>(stream)));
@@ -220,9 +219,6 @@ int sgemm_f8_quantize(int block, int format, int x_type, int64_t rows, int64_t c
     a.rows = (int)rows;
     a.cols = (int)cols;
     a.tiles_c = 0;
-    a.vec_x = ox.rows_on(16);
-    a.vec_q = Q && oq.rows_on(8);
-    a.vec_qt = QT && oqt.rows_on(8);
     (void)hipGetLastError();
     return finish(launch_f8_quantize(a, block == SGEMM_F8_TILE, format, x_type, reinterpret_cast<hipStream_t>(stream)));
 }
@@ -275,9 +271,6 @@ int sgemm_f8_rmsnorm(int type, int w_type, int64_t rows, int64_t cols, const voi
     a.cols = (int)cols;
     a.eps = eps;
     a.w_f32 = w_type == SGEMM_TYPE_F32;
-    a.vec = ox.rows_on(16) && (!R || orr.rows_on(16)) && (!H || oh.rows_on(16)) && (!Y || oy.rows_on(16)) &&
-            on(W, 16);
-    a.vec_q = Q && oq.rows_on(8);
     (void)hipGetLastError();
     return finish(launch_rmsnorm(a, type, reinterpret_cast<hipStream_t>(stream)));
 }
@@ -339,7 +332,6 @@ int sgemm_f8_rmsnorm_bwd(int type, int w_type, int64_t rows, int64_t cols, const
     a.cols = (int)cols;
     a.groups = (int)groups;
     a.w_f32 = w_type == SGEMM_TYPE_F32;
-    a.vec = ody.rows_on(16) && oh.rows_on(16) && (!DH || odh.rows_on(16)) && odx.rows_on(16) && on(W, 16);
     (void)hipGetLastError();
     return finish(launch_rmsnorm_bwd(a, type, reinterpret_cast<hipStream_t>(stream)));
 }

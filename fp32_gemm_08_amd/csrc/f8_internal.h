@@ -29,7 +29,6 @@ struct F8GemmArgs {
     int kb_split;                         // k-blocks per split
     float alpha, beta;
     int c_type;
-    int vec_c;                            // every row of C starts on a 16-byte boundary
 };
 
 struct F8GemmPlan {
@@ -52,7 +51,6 @@ struct F8QuantArgs {
     int64_t ldx, ldq, lds, ldqt, ldst;
     int rows, cols;
     int tiles_c;            // tiles along the columns
-    int vec_x, vec_q, vec_qt;
 };
 hipError_t launch_f8_quantize(F8QuantArgs a, bool tile, int format, int x_type, hipStream_t s);
 
@@ -65,8 +63,6 @@ struct NormArgs {
     int rows, cols;
     float eps;
     int w_f32;              // W is FP32 (else of the rows' type)
-    int vec;                // every row of X, R, H, Y (and W) allows 16-byte accesses
-    int vec_q;              // every row of Q allows 8-byte stores
 };
 hipError_t launch_rmsnorm(const NormArgs &a, int type, hipStream_t s);
 
@@ -77,7 +73,7 @@ struct NormBwdArgs {
     float *DW, *ws;         // ws: [groups][cols] partial sums of DW
     int64_t lddy, ldh, lddh, lddx;
     int rows, cols, groups;
-    int w_f32, vec;
+    int w_f32;
 };
 int64_t rmsnorm_bwd_groups(int64_t rows, int64_t cols);
 hipError_t launch_rmsnorm_bwd(const NormBwdArgs &a, int type, hipStream_t s);

@@ -30,12 +30,21 @@ __device__ __forceinline__ uint32_t f8_pack4(float a, float b, float c, float d)
     }
 }
 
+// Vectors at any address: the hardware's global loads and stores of up to 16
+// bytes take every byte alignment, so rows that start anywhere are accessed whole.
+typedef f8_f32x4 f8_f32x4_any __attribute__((aligned(1)));
+typedef f8_u32x2 f8_u32x2_any __attribute__((aligned(1)));
+typedef _Float16 f8_h8 __attribute__((ext_vector_type(8)));
+typedef __bf16 f8_b8 __attribute__((ext_vector_type(8)));
+typedef f8_h8 f8_h8_any __attribute__((aligned(1)));
+typedef f8_b8 f8_b8_any __attribute__((aligned(1)));
+
 // Row elements: loads and stores of 8 consecutive ones as FP32.
 template <typename T> struct Elt;
 template <> struct Elt<float> {
     static __device__ __forceinline__ void load8(const float *p, float (&v)[8])
     {
-        const f8_f32x4 a = *reinterpret_cast<const f8_f32x4 *>(p), b = *reinterpret_cast<const f8_f32x4 *>(p + 4);
+        const f8_f32x4 a = *reinterpret_cast<const f8_f32x4_any *>(p), b = *reinterpret_cast<const f8_f32x4_any *>(p + 4);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[i] = a[i];
@@ -44,16 +53,16 @@ template <> struct Elt<float> {
     }
     static __device__ __forceinline__ void store8(float *p, const float (&v)[8])
     {
-        *reinterpret_cast<f8_f32x4 *>(p) = f8_f32x4{v[0], v[1], v[2], v[3]};
-        *reinterpret_cast<f8_f32x4 *>(p + 4) = f8_f32x4{v[4], v[5], v[6], v[7]};
+        *reinterpret_cast<f8_f32x4_any *>(p) = f8_f32x4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<f8_f32x4_any *>(p + 4) = f8_f32x4{v[4], v[5], v[6], v[7]};
     }
     static __device__ __forceinline__ float get(const float *p) { return *p; }
     static __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 };
-template <typename T, typename V8> struct Elt16 {
+template <typename T, typename V8, typename V8any> struct Elt16 {
     static __device__ __forceinline__ void load8(const T *p, float (&v)[8])
     {
-        const V8 a = *reinterpret_cast<const V8 *>(p);
+        const V8 a = *reinterpret_cast<const V8any *>(p);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             v[i] = (float)a[i];
@@ -64,21 +73,19 @@ template <typename T, typename V8> struct Elt16 {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             a[i] = (T)v[i];
-        *reinterpret_cast<V8 *>(p) = a;
+        *reinterpret_cast<V8any *>(p) = a;
     }
     static __device__ __forceinline__ float get(const T *p) { return (float)*p; }
     static __device__ __forceinline__ void put(T *p, float v) { *p = (T)v; }
 };
-typedef _Float16 f8_h8 __attribute__((ext_vector_type(8)));
-typedef __bf16 f8_b8 __attribute__((ext_vector_type(8)));
-template <> struct Elt<_Float16> : Elt16<_Float16, f8_h8> {};
-template <> struct Elt<__bf16> : Elt16<__bf16, f8_b8> {};
+template <> struct Elt<_Float16> : Elt16<_Float16, f8_h8, f8_h8_any> {};
+template <> struct Elt<__bf16> : Elt16<__bf16, f8_b8, f8_b8_any> {};
 
 // Elements c .. c+7 of a row of `cols`, zero past its end.
 template <typename T>
-__device__ __forceinline__ void row_load8(const T *row, int c, int cols, bool vec, float (&v)[8])
+__device__ __forceinline__ void row_load8(const T *row, int c, int cols, float (&v)[8])
 {
-    if (vec && c + 8 <= cols) {
+    if (c + 8 <= cols) {
         Elt<T>::load8(row + c, v);
     } else {
 #pragma unroll
@@ -87,9 +94,9 @@ __device__ __forceinline__ void row_load8(const T *row, int c, int cols, bool ve
     }
 }
 template <typename T>
-__device__ __forceinline__ void row_store8(T *row, int c, int cols, bool vec, const float (&v)[8])
+__device__ __forceinline__ void row_store8(T *row, int c, int cols, const float (&v)[8])
 {
-    if (vec && c + 8 <= cols) {
+    if (c + 8 <= cols) {
         Elt<T>::store8(row + c, v);
     } else {
 #pragma unroll
@@ -99,10 +106,10 @@ __device__ __forceinline__ void row_store8(T *row, int c, int cols, bool vec, co
     }
 }
 // The same for 8 bytes held in two words.
-__device__ __forceinline__ void row_store8b(uint8_t *row, int c, int cols, bool vec, uint32_t lo, uint32_t hi)
+__device__ __forceinline__ void row_store8b(uint8_t *row, int c, int cols, uint32_t lo, uint32_t hi)
 {
-    if (vec && c + 8 <= cols) {
-        *reinterpret_cast<f8_u32x2 *>(row + c) = f8_u32x2{lo, hi};
+    if (c + 8 <= cols) {
+        *reinterpret_cast<f8_u32x2_any *>(row + c) = f8_u32x2{lo, hi};
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)

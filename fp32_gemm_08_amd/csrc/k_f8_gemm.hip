@@ -38,12 +38,12 @@ __device__ __forceinline__ void put8(const F8GemmArgs &g, int m, int n, const fl
         o[i] = g.alpha * v[i];
     if (g.beta != 0.0f) {
         float old[8];
-        row_load8(row, n, g.N, g.vec_c, old);
+        row_load8(row, n, g.N, old);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             o[i] = fmaf(g.beta, old[i], o[i]);
     }
-    row_store8(row, n, g.N, g.vec_c, o);
+    row_store8(row, n, g.N, o);
 }
 
 // A wavefront's 16 rows of WN columns of C, of which lane l holds row l % 16,

@@ -7,9 +7,10 @@
 // an 8 x 8 piece of it (8 consecutive rows, 8 consecutive columns).  The 16
 // lanes of a data-parallel row hold one row of the tile, so a row block's
 // maximum is four lane permutations; a column block's maximum crosses the
-// wavefronts through 2 KB of LDS.  The transposed output goes through an LDS
-// tile of bytes: a work-item's 8 rows of one column are 8 consecutive bytes of
-// it.  X is read once, each output is written once.
+// wavefronts through 2 KB of LDS.  One work-item divides for each row and each
+// column, and the factors go round through the LDS.  The transposed output goes
+// through an LDS tile of bytes: a work-item's 8 rows of one column are 8
+// consecutive bytes of it.  X is read once, each output is written once.
 #include "f8_types.h"
 
 namespace sgemm {
@@ -24,6 +25,7 @@ __global__ __launch_bounds__(256) void f8_quantize_kernel(F8QuantArgs g)
     __shared__ __attribute__((aligned(16))) uint8_t tile[QT * QT_PITCH];
     __shared__ uint32_t colmax[4][QT];
     __shared__ uint32_t wavemax[4];
+    __shared__ __attribute__((aligned(16))) float factor[2][QT];  // of the rows, of the columns
     poison_lds(tile, (int)sizeof(tile));
 
     const int tr = blockIdx.x / g.tiles_c, tc = blockIdx.x % g.tiles_c;
@@ -37,7 +39,7 @@ __global__ __launch_bounds__(256) void f8_quantize_kernel(F8QuantArgs g)
     for (int i = 0; i < 8; ++i) {
         const int r = r0 + pr + i;
         if (r < g.rows && c < g.cols) {
-            row_load8(static_cast<const T *>(g.X) + (int64_t)r * g.ldx, c, g.cols, g.vec_x, v[i]);
+            row_load8(static_cast<const T *>(g.X) + (int64_t)r * g.ldx, c, g.cols, v[i]);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -71,11 +73,19 @@ __global__ __launch_bounds__(256) void f8_quantize_kernel(F8QuantArgs g)
         }
     } else {
         if (g.Q) {
+            // the lane i of a row of 16 takes the row pr + i
+            uint32_t m = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                float scale;
-                block_scale<FMT>(max16(abs_max8(v[i])), inv_r[i], scale);
-                if (pc == 0 && r0 + pr + i < g.rows)
+                const uint32_t mi = max16(abs_max8(v[i]));
+                m = threadIdx.x % 16 == i ? mi : m;
+            }
+            const int i = threadIdx.x % 16;
+            if (i < 8) {
+                float inv, scale;
+                block_scale<FMT>(m, inv, scale);
+                factor[0][pr + i] = inv;
+                if (r0 + pr + i < g.rows)
                     g.S[(int64_t)tc * g.lds + r0 + pr + i] = scale;
             }
         }
@@ -96,15 +106,20 @@ __global__ __launch_bounds__(256) void f8_quantize_kernel(F8QuantArgs g)
                     colmax[w][pc + j] = m[j];
             }
             __syncthreads();
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float scale;
-                const uint32_t mm = max(max(colmax[0][pc + j], colmax[1][pc + j]),
-                                        max(colmax[2][pc + j], colmax[3][pc + j]));
-                block_scale<FMT>(mm, inv_c[j], scale);
-                if (threadIdx.x < 16 && c + j < g.cols)
-                    g.ST[(int64_t)tr * g.ldst + c + j] = scale;
+            if (threadIdx.x < QT) {
+                const int t = threadIdx.x;
+                float inv, scale;
+                block_scale<FMT>(max(max(colmax[0][t], colmax[1][t]), max(colmax[2][t], colmax[3][t])), inv, scale);
+                factor[1][t] = inv;
+                if (c0 + t < g.cols)
+                    g.ST[(int64_t)tr * g.ldst + c0 + t] = scale;
             }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            inv_r[i] = factor[0][pr + i];
+            inv_c[i] = factor[1][pc + i];
         }
     }
 
@@ -116,7 +131,7 @@ __global__ __launch_bounds__(256) void f8_quantize_kernel(F8QuantArgs g)
             const uint32_t lo = f8_pack4<FMT>(v[i][0] * f, v[i][1] * f, v[i][2] * f, v[i][3] * f);
             const uint32_t hi = f8_pack4<FMT>(v[i][4] * f, v[i][5] * f, v[i][6] * f, v[i][7] * f);
             if (r < g.rows && c < g.cols)
-                row_store8b(g.Q + (int64_t)r * g.ldq, c, g.cols, g.vec_q, lo, hi);
+                row_store8b(g.Q + (int64_t)r * g.ldq, c, g.cols, lo, hi);
         }
     }
     if (g.QT) {
@@ -134,7 +149,7 @@ __global__ __launch_bounds__(256) void f8_quantize_kernel(F8QuantArgs g)
             const int col = 16 * i + threadIdx.x / 16, at = 8 * (threadIdx.x % 16);
             if (c0 + col < g.cols && r0 + at < g.rows) {
                 const f8_u32x2 x = *reinterpret_cast<const f8_u32x2 *>(tile + col * QT_PITCH + at);
-                row_store8b(g.QT + (int64_t)(c0 + col) * g.ldqt, r0 + at, g.rows, g.vec_qt, x[0], x[1]);
+                row_store8b(g.QT + (int64_t)(c0 + col) * g.ldqt, r0 + at, g.rows, x[0], x[1]);
             }
         }
     }

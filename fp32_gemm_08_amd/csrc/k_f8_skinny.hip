@@ -10,13 +10,14 @@ template <typename T>
 __device__ __forceinline__ void put4(const F8GemmArgs &g, int m, int n, f8_f32x4 v)
 {
     typedef T V4 __attribute__((ext_vector_type(4)));
+    typedef V4 V4any __attribute__((aligned(1)));
     T *p = static_cast<T *>(g.C) + (int64_t)m * g.ldc + n;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         v[i] *= g.alpha;
-    if (g.vec_c && n + 4 <= g.N) {
+    if (n + 4 <= g.N) {
         if (g.beta != 0.0f) {
-            const V4 old = *reinterpret_cast<const V4 *>(p);
+            const V4 old = *reinterpret_cast<const V4any *>(p);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 v[i] = fmaf(g.beta, (float)old[i], v[i]);
@@ -25,7 +26,7 @@ __device__ __forceinline__ void put4(const F8GemmArgs &g, int m, int n, f8_f32x4
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             o[i] = (T)v[i];
-        *reinterpret_cast<V4 *>(p) = o;
+        *reinterpret_cast<V4any *>(p) = o;
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)

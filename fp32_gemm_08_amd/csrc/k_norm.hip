@@ -35,12 +35,12 @@ __device__ __forceinline__ float group_sum(float v, float *slot)
 }
 
 template <typename T>
-__device__ __forceinline__ void load_w8(const void *W, int w_f32, int c, int cols, bool vec, float (&v)[8])
+__device__ __forceinline__ void load_w8(const void *W, int w_f32, int c, int cols, float (&v)[8])
 {
     if (w_f32)
-        row_load8(static_cast<const float *>(W), c, cols, vec, v);
+        row_load8(static_cast<const float *>(W), c, cols, v);
     else
-        row_load8(static_cast<const T *>(W), c, cols, vec, v);
+        row_load8(static_cast<const T *>(W), c, cols, v);
 }
 
 template <typename T, int NT, int V>
@@ -54,10 +54,10 @@ __global__ __launch_bounds__(NT) void rmsnorm_kernel(NormArgs g)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = 8 * (threadIdx.x + NT * i);
-        row_load8(x, c, g.cols, g.vec, h[i]);
+        row_load8(x, c, g.cols, h[i]);
         if (g.R) {
             float r[8];
-            row_load8(static_cast<const T *>(g.R) + row * g.ldr, c, g.cols, g.vec, r);
+            row_load8(static_cast<const T *>(g.R) + row * g.ldr, c, g.cols, r);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 h[i][j] += r[j];
@@ -66,7 +66,7 @@ __global__ __launch_bounds__(NT) void rmsnorm_kernel(NormArgs g)
         for (int j = 0; j < 8; ++j)
             ss = fmaf(h[i][j], h[i][j], ss);
         if (g.H && c < g.cols)
-            row_store8(static_cast<T *>(g.H) + row * g.ldh, c, g.cols, g.vec, h[i]);
+            row_store8(static_cast<T *>(g.H) + row * g.ldh, c, g.cols, h[i]);
     }
     ss = group_sum<NT>(ss, slot);
     const float rstd = 1.0f / sqrtf(ss / (float)g.cols + g.eps);
@@ -78,19 +78,19 @@ __global__ __launch_bounds__(NT) void rmsnorm_kernel(NormArgs g)
     for (int i = 0; i < V; ++i) {
         const int c = 8 * (threadIdx.x + NT * i);
         float w[8], y[8];
-        load_w8<T>(g.W, g.w_f32, c, g.cols, g.vec, w);
+        load_w8<T>(g.W, g.w_f32, c, g.cols, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             y[j] = c + j < g.cols ? h[i][j] * rstd * w[j] : 0.0f;
         if (g.Y && c < g.cols)
-            row_store8(static_cast<T *>(g.Y) + row * g.ldy, c, g.cols, g.vec, y);
+            row_store8(static_cast<T *>(g.Y) + row * g.ldy, c, g.cols, y);
         if (g.Q) {
             float inv, scale;
             block_scale<0>(max16(abs_max8(y)), inv, scale);
             if (c < g.cols) {
                 const uint32_t lo = f8_pack4<0>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
                 const uint32_t hi = f8_pack4<0>(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
-                row_store8b(g.Q + row * g.ldq, c, g.cols, g.vec_q, lo, hi);
+                row_store8b(g.Q + row * g.ldq, c, g.cols, lo, hi);
                 if ((threadIdx.x & 15) == 0)
                     g.S[(int64_t)(c / F8_BLOCK) * g.lds + row] = scale;
             }
@@ -105,7 +105,7 @@ __global__ __launch_bounds__(NT) void rmsnorm_bwd_kernel(NormBwdArgs g)
     float dw[V][8], w[V][8];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        load_w8<T>(g.W, g.w_f32, 8 * (threadIdx.x + NT * i), g.cols, g.vec, w[i]);
+        load_w8<T>(g.W, g.w_f32, 8 * (threadIdx.x + NT * i), g.cols, w[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             dw[i][j] = 0.0f;
@@ -118,8 +118,8 @@ __global__ __launch_bounds__(NT) void rmsnorm_bwd_kernel(NormBwdArgs g)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = 8 * (threadIdx.x + NT * i);
-            row_load8(static_cast<const T *>(g.DY) + row * g.lddy, c, g.cols, g.vec, dy[i]);
-            row_load8(static_cast<const T *>(g.H) + row * g.ldh, c, g.cols, g.vec, n[i]);
+            row_load8(static_cast<const T *>(g.DY) + row * g.lddy, c, g.cols, dy[i]);
+            row_load8(static_cast<const T *>(g.H) + row * g.ldh, c, g.cols, n[i]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 n[i][j] *= rstd;
@@ -139,21 +139,20 @@ __global__ __launch_bounds__(NT) void rmsnorm_bwd_kernel(NormBwdArgs g)
                 dx[j] = rstd * (dy[i][j] * w[i][j] - n[i][j] * mean);
             if (g.DH) {
                 float dh[8];
-                row_load8(static_cast<const T *>(g.DH) + row * g.lddh, c, g.cols, g.vec, dh);
+                row_load8(static_cast<const T *>(g.DH) + row * g.lddh, c, g.cols, dh);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     dx[j] += dh[j];
             }
-            row_store8(static_cast<T *>(g.DX) + row * g.lddx, c, g.cols, g.vec, dx);
+            row_store8(static_cast<T *>(g.DX) + row * g.lddx, c, g.cols, dx);
         }
     }
     if (g.DW) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = 8 * (threadIdx.x + NT * i);
-            // the workspace's rows are whole multiples of 8 long only where cols is
             if (c < g.cols)
-                row_store8(g.ws + (int64_t)blockIdx.x * g.cols, c, g.cols, g.cols % 8 == 0, dw[i]);
+                row_store8(g.ws + (int64_t)blockIdx.x * g.cols, c, g.cols, dw[i]);
         }
     }
 }

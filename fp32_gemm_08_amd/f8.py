@@ -97,12 +97,14 @@ def sgemm_f8_rmsnorm_bwd_plan(rows, cols):
 _FORMAT_OF = None  # torch dtype -> sgemm_f8_format; -> sgemm_type; FP32 alone
 _TYPE_OF = None
 _F32 = None
+_raw_stream = _current_device = None
 
 
 def _tables():
-    global _FORMAT_OF, _TYPE_OF, _F32
+    global _FORMAT_OF, _TYPE_OF, _F32, _raw_stream, _current_device
     import torch
 
+    _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
     _FORMAT_OF = {torch.float8_e4m3fn: 1, torch.float8_e5m2: 2}
     _TYPE_OF = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
     _F32 = {torch.float32: 0}
@@ -112,30 +114,32 @@ def _matrix(name, t, table, device):
     """(id of the element type, rows, cols, address, leading dimension) of a
     2-D device tensor with unit stride along its rows."""
     kind = table.get(t.dtype)
-    if kind is None or t.dim() != 2 or t.device != device or not t.is_cuda:
+    if kind is None or t.dim() != 2 or t.device != device:
         raise TypeError(f"{name}: a 2-D {' / '.join(str(k)[6:] for k in table)} tensor on the call's device is needed")
     rows, cols = t.shape
     ld, step = t.stride()
-    if cols > 1 and step != 1:
+    if step != 1 and cols > 1:
         raise ValueError(f"{name} must have unit stride along its last dimension")
-    if rows <= 1 or ld == 0 and cols == 0:
-        ld = max(cols, 1)
-    elif ld < cols:
-        raise ValueError(f"{name} rows overlap (row stride below the row length)")
-    return kind, rows, cols, t.data_ptr(), max(ld, 1)
+    if ld < cols or ld == 0:
+        if rows > 1 and cols > 0:
+            raise ValueError(f"{name} rows overlap (row stride below the row length)")
+        ld = cols or 1
+    elif rows <= 1:
+        ld = cols or 1
+    return kind, rows, cols, t.data_ptr(), ld
 
 
 def _scale(name, t, shape, device):
     """(address, leading dimension) of an FP32 array of scales of that shape."""
     _, rows, cols, p, ld = _matrix(name, t, _F32, device)
-    if (rows, cols) != shape:
+    if rows != shape[0] or cols != shape[1]:
         raise ValueError(f"{name} has shape {(rows, cols)}, not {shape}")
     return p, ld
 
 
 def _vector(name, t, n, device, types):
     kind = types.get(t.dtype)
-    if kind is None or t.dim() != 1 or t.device != device or not t.is_cuda:
+    if kind is None or t.dim() != 1 or t.device != device:
         raise TypeError(f"{name}: a 1-D {' / '.join(str(k)[6:] for k in types)} tensor on the call's device is needed")
     if t.shape[0] != n or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must hold {n} consecutive values")
@@ -158,16 +162,27 @@ def _scale_shape(block, rows, cols):
     return (_blocks(cols), rows) if block == 0 else (_blocks(rows), _blocks(cols))
 
 
-def _run(device, stream, fn, args):
-    import torch
+def _device(t):
+    """The device of a call: that of its first tensor, which must be a GPU."""
+    if _FORMAT_OF is None:
+        _tables()
+    dev = t.device
+    if dev.type != "cuda":
+        raise TypeError("tensors on a GPU are needed")
+    return dev
 
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, stream.cuda_stream)
+
+def _run(device, stream, fn, args):
+    # the raw handle of torch's current stream: the Stream object around it
+    # costs 2 us, as much as the launch itself
+    raw = _raw_stream(device.index) if stream is None else stream.cuda_stream
+    if _current_device() == device.index:
+        st = fn(*args, raw)
     else:
+        import torch
+
         with torch.cuda.device(device):
-            st = fn(*args, stream.cuda_stream)
+            st = fn(*args, raw)
     if st != SGEMM_OK:
         raise SgemmError(st, sgemm_f32_status_string(st))
 
@@ -183,9 +198,7 @@ def f8_gemm(A, SA, B, SB, C, alpha=1.0, beta=0.0, b_scale="tile", workspace=None
     for partial sums where few output tiles make it worthwhile
     (sgemm_f8_gemm_plan says how much is used).
     """
-    if _FORMAT_OF is None:
-        _tables()
-    dev = C.device
+    dev = _device(C)
     block = F8_BLOCK[b_scale]
     fa, M, K, pa, lda = _matrix("A", A, _FORMAT_OF, dev)
     fb, N, kb, pb, ldb = _matrix("B", B, _FORMAT_OF, dev)
@@ -209,9 +222,7 @@ def f8_quantize(X, Q=None, S=None, QT=None, ST=None, block="row", stream=None):
     per 128 x 128, S (ceil(rows/128), ceil(cols/128)), ST its transpose.  The
     format is Q's (and QT's) type.
     """
-    if _FORMAT_OF is None:
-        _tables()
-    dev = X.device
+    dev = _device(X)
     b = F8_BLOCK[block]
     xt, rows, cols, px, ldx = _matrix("X", X, _TYPE_OF, dev)
     fmt = fq = fqt = 0
@@ -248,9 +259,7 @@ def rmsnorm(X, W, eps=1e-6, residual=None, H=None, Y=None, Q=None, S=None, rstd=
     (ceil(cols/128), rows) <- y in 8 bits, rstd (rows, float32) for the backward
     pass.
     """
-    if _FORMAT_OF is None:
-        _tables()
-    dev = X.device
+    dev = _device(X)
     t, rows, cols, px, ldx = _matrix("X", X, _TYPE_OF, dev)
     wt, pw = _vector("W", W, cols, dev, _TYPE_OF)
     if wt != t and wt != 0:
@@ -289,9 +298,7 @@ def rmsnorm_backward(dY, H, W, rstd, dX, dW=None, workspace=None, dH=None, strea
     dH or H itself.  dW (cols, float32) needs a ``workspace`` of
     sgemm_f8_rmsnorm_bwd_plan's bytes.
     """
-    if _FORMAT_OF is None:
-        _tables()
-    dev = dY.device
+    dev = _device(dY)
     t, rows, cols, pdy, lddy = _matrix("dY", dY, _TYPE_OF, dev)
     wt, pw = _vector("W", W, cols, dev, _TYPE_OF)
     if wt != t and wt != 0:

@@ -42,6 +42,15 @@ typedef f8_b8 f8_b8_any __attribute__((aligned(1)));
 // Row elements: loads and stores of 8 consecutive ones as FP32.
 template <typename T> struct Elt;
 template <> struct Elt<float> {
+    struct Raw {
+        f8_f32x4 a, b;
+        __device__ __forceinline__ float operator[](int i) const { return i < 4 ? a[i] : b[i - 4]; }
+    };
+    static __device__ __forceinline__ Raw raw8(const float *p)
+    {
+        return {*reinterpret_cast<const f8_f32x4_any *>(p), *reinterpret_cast<const f8_f32x4_any *>(p + 4)};
+    }
+    static __device__ __forceinline__ void set(Raw &r, int i, float v) { i < 4 ? r.a[i] = v : r.b[i - 4] = v; }
     static __device__ __forceinline__ void load8(const float *p, float (&v)[8])
     {
         const f8_f32x4 a = *reinterpret_cast<const f8_f32x4_any *>(p), b = *reinterpret_cast<const f8_f32x4_any *>(p + 4);
@@ -60,6 +69,9 @@ template <> struct Elt<float> {
     static __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 };
 template <typename T, typename V8, typename V8any> struct Elt16 {
+    typedef V8 Raw;
+    static __device__ __forceinline__ Raw raw8(const T *p) { return *reinterpret_cast<const V8any *>(p); }
+    static __device__ __forceinline__ void set(Raw &r, int i, T v) { r[i] = v; }
     static __device__ __forceinline__ void load8(const T *p, float (&v)[8])
     {
         const V8 a = *reinterpret_cast<const V8any *>(p);
@@ -92,6 +104,19 @@ __device__ __forceinline__ void row_load8(const T *row, int c, int cols, float (
         for (int i = 0; i < 8; ++i)
             v[i] = c + i < cols ? Elt<T>::get(row + c + i) : 0.0f;
     }
+}
+// The same, unconverted (values requested ahead stay in as few registers as they have bytes).
+template <typename T>
+__device__ __forceinline__ typename Elt<T>::Raw row_raw8(const T *row, int c, int cols)
+{
+    if (c + 8 <= cols)
+        return Elt<T>::raw8(row + c);
+    typename Elt<T>::Raw r{};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (c + i < cols)
+            Elt<T>::set(r, i, row[c + i]);
+    return r;
 }
 template <typename T>
 __device__ __forceinline__ void row_store8(T *row, int c, int cols, const float (&v)[8])
@@ -144,12 +169,20 @@ __device__ __forceinline__ uint32_t max16(uint32_t m)
     return m;
 }
 
-// Sum over the 64 lanes of a wavefront, in every lane.
-__device__ __forceinline__ float wave_sum(float v)
+// Sum over each aligned group of L lanes (16, 32 or 64), in every lane of the
+// group: the same butterfly, and exchanges between the groups of 16.
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v)
 {
-#pragma unroll
-    for (int off = 32; off; off >>= 1)
-        v += __shfl_xor(v, off);
+    static_assert(L == 16 || L == 32 || L == 64, "whole groups of 16 lanes");
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xf, 0xf, false));
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xf, 0xf, false));
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xf, 0xf, false));
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xf, 0xf, false));
+    if constexpr (L >= 32)
+        v += __shfl_xor(v, 16);
+    if constexpr (L == 64)
+        v += __shfl_xor(v, 32);
     return v;
 }
 

@@ -1,36 +1,39 @@
 // Root-mean-square norm with the residual's addition and an 8-bit output, and
 // its backward pass.
 //
-// Forward: a workgroup of NT work-items per row, each holding V pieces of 8
-// consecutive columns in registers between the sum of squares and the output,
-// so each row is read once.  16 consecutive lanes hold one block of 128
-// columns, whose maximum is four lane permutations.
+// L work-items hold a row, each V pieces of 8 consecutive columns in registers,
+// so each row is read once: a workgroup takes one row (L = NT) or, of rows of up
+// to 512 columns, NT / L at a time (16, 32 or 64 lanes a row).  16 consecutive
+// lanes hold one block of 128 columns, whose maximum is four lane permutations.
 //
 // Backward: with n = h * rstd and g = dy * w,
 //     dx = rstd * (g - n * mean(g n)) + dh,      dw = sum over rows of dy n.
-// A workgroup walks the rows blockIdx.x, blockIdx.x + groups, ...; each
+// A workgroup walks the rows, a stride of all workgroups' rows apart; each
 // work-item keeps the sums of dw for its columns in registers, and a second
 // kernel adds the workgroups' sums in a fixed order.
 #include "f8_types.h"
 
+#include <algorithm>
+
 namespace sgemm {
 namespace {
 
-// Sum of `v` over the workgroup, in every work-item.  `slot` has NT/64 floats
-// that no other sum uses at the same time.
-template <int NT>
-__device__ __forceinline__ float group_sum(float v, float *slot)
+// Sum of `v` over the work-items of a row, in every one of them.  `slot` has
+// NT/64 floats that no other sum uses at the same time.
+template <int NT, int L>
+__device__ __forceinline__ float row_sum(float v, float *slot)
 {
-    v = wave_sum(v);
-    if constexpr (NT > 64) {
-        if ((threadIdx.x & 63) == 0)
-            slot[threadIdx.x >> 6] = v;
-        __syncthreads();
-        v = 0.0f;
+    if constexpr (L <= 64)
+        return lanes_sum<L>(v);
+    static_assert(L <= 64 || L == NT, "a row of several wavefronts is the workgroup's only one");
+    v = lanes_sum<64>(v);
+    if ((threadIdx.x & 63) == 0)
+        slot[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NT / 64; ++i)
-            v += slot[i];
-    }
+    for (int i = 0; i < NT / 64; ++i)
+        v += slot[i];
     return v;
 }
 
@@ -43,17 +46,20 @@ __device__ __forceinline__ void load_w8(const void *W, int w_f32, int c, int col
         row_load8(static_cast<const T *>(W), c, cols, v);
 }
 
-template <typename T, int NT, int V>
+template <typename T, int NT, int L, int V>
 __global__ __launch_bounds__(NT) void rmsnorm_kernel(NormArgs g)
 {
     __shared__ float slot[NT / 64];
-    const int64_t row = blockIdx.x;
+    const int lane = threadIdx.x % L;                                    // of the row's
+    const int64_t row = (int64_t)blockIdx.x * (NT / L) + threadIdx.x / L;
+    if (row >= g.rows)
+        return;  // whole rows of lanes, and only where no row needs the workgroup
     const T *x = static_cast<const T *>(g.X) + row * g.ldx;
     float h[V][8];
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int c = 8 * (threadIdx.x + NT * i);
+        const int c = 8 * (lane + L * i);
         row_load8(x, c, g.cols, h[i]);
         if (g.R) {
             float r[8];
@@ -68,15 +74,15 @@ __global__ __launch_bounds__(NT) void rmsnorm_kernel(NormArgs g)
         if (g.H && c < g.cols)
             row_store8(static_cast<T *>(g.H) + row * g.ldh, c, g.cols, h[i]);
     }
-    ss = group_sum<NT>(ss, slot);
+    ss = row_sum<NT, L>(ss, slot);
     const float rstd = 1.0f / sqrtf(ss / (float)g.cols + g.eps);
-    if (g.rstd && threadIdx.x == 0)
+    if (g.rstd && lane == 0)
         g.rstd[row] = rstd;
     if (!g.Y && !g.Q)
         return;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int c = 8 * (threadIdx.x + NT * i);
+        const int c = 8 * (lane + L * i);
         float w[8], y[8];
         load_w8<T>(g.W, g.w_f32, c, g.cols, w);
 #pragma unroll
@@ -98,67 +104,109 @@ __global__ __launch_bounds__(NT) void rmsnorm_kernel(NormArgs g)
     }
 }
 
-template <typename T, int NT, int V>
+// AHEAD: the next row's values are requested before this row's are used.
+template <typename T, int NT, int L, int V, bool AHEAD>
 __global__ __launch_bounds__(NT) void rmsnorm_bwd_kernel(NormBwdArgs g)
 {
+    typedef typename Elt<T>::Raw Raw;
+    constexpr int ROWS = NT / L;
     __shared__ float slot[2][NT / 64];
+    __shared__ float sums[ROWS > 1 ? NT * 8 : 1];
+    const int lane = threadIdx.x % L, own = threadIdx.x / L;
     float dw[V][8], w[V][8];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        load_w8<T>(g.W, g.w_f32, 8 * (threadIdx.x + NT * i), g.cols, w[i]);
+        load_w8<T>(g.W, g.w_f32, 8 * (lane + L * i), g.cols, w[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             dw[i][j] = 0.0f;
     }
-    int turn = 0;
-    for (int64_t row = blockIdx.x; row < g.rows; row += g.groups, turn ^= 1) {
+    Raw dy[V], h[V], dh[V];
+    Raw ady[AHEAD ? V : 1], ah[AHEAD ? V : 1], adh[AHEAD ? V : 1];  // the next row's
+    auto request = [&](int64_t row, Raw *to_dy, Raw *to_h, Raw *to_dh) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = 8 * (lane + L * i);
+            to_dy[i] = row_raw8(static_cast<const T *>(g.DY) + row * g.lddy, c, g.cols);
+            to_h[i] = row_raw8(static_cast<const T *>(g.H) + row * g.ldh, c, g.cols);
+            if (g.DH)
+                to_dh[i] = row_raw8(static_cast<const T *>(g.DH) + row * g.lddh, c, g.cols);
+        }
+    };
+    const int64_t step = (int64_t)g.groups * ROWS;
+    int64_t row = (int64_t)blockIdx.x * ROWS + own;
+    if (AHEAD && row < g.rows)
+        request(row, ady, ah, adh);
+    for (int turn = 0; row < g.rows; row += step, turn ^= 1) {
         const float rstd = g.rstd[row];
-        float dy[V][8], n[V][8];
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                dy[i] = ady[i];
+                h[i] = ah[i];
+                dh[i] = adh[i];
+            }
+            if (row + step < g.rows)
+                request(row + step, ady, ah, adh);
+        } else {
+            request(row, dy, h, dh);
+        }
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = 8 * (threadIdx.x + NT * i);
-            row_load8(static_cast<const T *>(g.DY) + row * g.lddy, c, g.cols, dy[i]);
-            row_load8(static_cast<const T *>(g.H) + row * g.ldh, c, g.cols, n[i]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                n[i][j] *= rstd;
-                sum = fmaf(dy[i][j] * w[i][j], n[i][j], sum);
-                dw[i][j] = fmaf(dy[i][j], n[i][j], dw[i][j]);
+                const float d = (float)dy[i][j], n = (float)h[i][j] * rstd;
+                sum = fmaf(d * w[i][j], n, sum);
+                dw[i][j] = fmaf(d, n, dw[i][j]);
             }
         }
-        const float mean = group_sum<NT>(sum, slot[turn]) / (float)g.cols;
+        const float mean = row_sum<NT, L>(sum, slot[turn]) / (float)g.cols;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = 8 * (threadIdx.x + NT * i);
+            const int c = 8 * (lane + L * i);
             if (c >= g.cols)
                 continue;
             float dx[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                dx[j] = rstd * (dy[i][j] * w[i][j] - n[i][j] * mean);
-            if (g.DH) {
-                float dh[8];
-                row_load8(static_cast<const T *>(g.DH) + row * g.lddh, c, g.cols, dh);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    dx[j] += dh[j];
+            for (int j = 0; j < 8; ++j) {
+                dx[j] = rstd * ((float)dy[i][j] * w[i][j] - (float)h[i][j] * rstd * mean);
+                if (g.DH)
+                    dx[j] += (float)dh[i][j];
             }
             row_store8(static_cast<T *>(g.DX) + row * g.lddx, c, g.cols, dx);
         }
     }
-    if (g.DW) {
+    if (!g.DW)
+        return;
+    float *out = g.ws + (int64_t)blockIdx.x * g.cols;
+    if constexpr (ROWS == 1) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = 8 * (threadIdx.x + NT * i);
+            const int c = 8 * (lane + L * i);
             if (c < g.cols)
-                row_store8(g.ws + (int64_t)blockIdx.x * g.cols, c, g.cols, dw[i]);
+                row_store8(out, c, g.cols, dw[i]);
+        }
+    } else {
+        // the workgroup's rows of lanes, in order
+        static_assert(V == 1, "one piece a lane");
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            sums[(own * 8 + j) * L + lane] = dw[0][j];
+        __syncthreads();
+        for (int c = threadIdx.x; c < g.cols; c += NT) {
+            float s = 0.0f;
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r)
+                s += sums[(r * 8 + c % 8) * L + c / 8];
+            out[c] = s;
         }
     }
 }
 
 // dw[c] = sum over the workgroups' partial sums, 32 columns and 32 strips of
-// partial sums per workgroup, in a fixed order.
+// partial sums per workgroup, in a fixed order; 8 loads of a strip at a time,
+// which is what its time is made of.
 __global__ __launch_bounds__(1024) void rmsnorm_dw_kernel(const float *ws, int groups, int cols, float *dw)
 {
     __shared__ float part[32][33];
@@ -166,49 +214,80 @@ __global__ __launch_bounds__(1024) void rmsnorm_dw_kernel(const float *ws, int g
     const int c = blockIdx.x * 32 + x;
     float s = 0.0f;
     if (c < cols)
-        for (int i = y; i < groups; i += 32)
-            s += ws[(int64_t)i * cols + c];
+        for (int i = y; i < groups; i += 8 * 32) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = i + 32 * j < groups ? ws[(int64_t)(i + 32 * j) * cols + c] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                s += v[j];
+        }
     part[y][x] = s;
     __syncthreads();
     if (y == 0 && c < cols) {
         s = 0.0f;
+#pragma unroll
         for (int i = 0; i < 32; ++i)
             s += part[i][x];
         dw[c] = s;
     }
 }
 
-// Work-items per row and pieces per work-item that cover `cols`.
+// Calls f.run<T, NT, L, V> with what covers `cols`: work-items of a workgroup
+// and of a row, and pieces per work-item.
 template <typename T, typename F>
 void by_cols(int cols, F f)
 {
-    if (cols <= 512)
-        f.template run<T, 64, 1>();
+    if (cols <= 128)
+        f.template run<T, 256, 16, 1>();
+    else if (cols <= 256)
+        f.template run<T, 256, 32, 1>();
+    else if (cols <= 512)
+        f.template run<T, 256, 64, 1>();
     else if (cols <= 1024)
-        f.template run<T, 128, 1>();
+        f.template run<T, 128, 128, 1>();
     else if (cols <= 2048)
-        f.template run<T, 256, 1>();
+        f.template run<T, 256, 256, 1>();
     else if (cols <= 4096)
-        f.template run<T, 256, 2>();
+        f.template run<T, 256, 256, 2>();
     else if (cols <= 8192)
-        f.template run<T, 512, 2>();
+        f.template run<T, 512, 512, 2>();
     else if (cols <= 16384)
-        f.template run<T, 1024, 2>();
+        f.template run<T, 1024, 1024, 2>();
     else
-        f.template run<T, 1024, 4>();
+        f.template run<T, 1024, 1024, 4>();
 }
 
 struct Fwd {
     const NormArgs &a;
     hipStream_t s;
-    template <typename T, int NT, int V> void run() { rmsnorm_kernel<T, NT, V><<<(unsigned)a.rows, NT, 0, s>>>(a); }
+    template <typename T, int NT, int L, int V> void run()
+    {
+        constexpr int64_t ROWS = NT / L;
+        rmsnorm_kernel<T, NT, L, V><<<(unsigned)((a.rows + ROWS - 1) / ROWS), NT, 0, s>>>(a);
+    }
 };
 struct Bwd {
     const NormBwdArgs &a;
     hipStream_t s;
-    template <typename T, int NT, int V> void run()
+    template <typename T, int NT, int L, int V> void run()
     {
-        rmsnorm_bwd_kernel<T, NT, V><<<(unsigned)a.groups, NT, 0, s>>>(a);
+        // with 1024 work-items of 128 registers, the 32-bit rows leave no room for the next one
+        constexpr bool AHEAD = NT < 1024 || (V == 2 && sizeof(T) == 2);
+        rmsnorm_bwd_kernel<T, NT, L, V, AHEAD><<<(unsigned)a.groups, NT, 0, s>>>(a);
+    }
+};
+// Workgroups of the backward pass: 8 wavefronts per CU (measured with 4 / 8 / 16
+// on rows of 4096 bf16: 122.6 / 105.5 / 114.8 us, of 1024: 166 / 106 / 112; of
+// few rows, one for each: 11.9 us on 1000 rows, 14.8 with 8 rows to a workgroup).
+struct Groups {
+    int64_t rows;
+    int64_t *out;
+    template <typename T, int NT, int L, int V> void run()
+    {
+        constexpr int64_t ROWS = NT / L, MOST = NT >= 512 ? 256 : 131072 / NT;
+        *out = std::min((rows + ROWS - 1) / ROWS, MOST);
     }
 };
 
@@ -233,8 +312,9 @@ hipError_t launch_rmsnorm(const NormArgs &a, int type, hipStream_t s)
 
 int64_t rmsnorm_bwd_groups(int64_t rows, int64_t cols)
 {
-    (void)cols;
-    return rows < 1024 ? rows : 1024;
+    int64_t n = 0;
+    by_cols<float>((int)cols, Groups{rows, &n});
+    return n;
 }
 
 hipError_t launch_rmsnorm_bwd(const NormBwdArgs &a, int type, hipStream_t s)

@@ -36,8 +36,6 @@ typedef f8_f32x4 f8_f32x4_any __attribute__((aligned(1)));
 typedef f8_u32x2 f8_u32x2_any __attribute__((aligned(1)));
 typedef _Float16 f8_h8 __attribute__((ext_vector_type(8)));
 typedef __bf16 f8_b8 __attribute__((ext_vector_type(8)));
-typedef f8_h8 f8_h8_any __attribute__((aligned(1)));
-typedef f8_b8 f8_b8_any __attribute__((aligned(1)));
 
 // Row elements: loads and stores of 8 consecutive ones as FP32.
 template <typename T> struct Elt;
@@ -51,13 +49,33 @@ template <> struct Elt<float> {
         return {*reinterpret_cast<const f8_f32x4_any *>(p), *reinterpret_cast<const f8_f32x4_any *>(p + 4)};
     }
     static __device__ __forceinline__ void set(Raw &r, int i, float v) { i < 4 ? r.a[i] = v : r.b[i - 4] = v; }
-    static __device__ __forceinline__ void load8(const float *p, float (&v)[8])
+    // Elements s .. 7 moved to the front, zeros behind them (s = 1 .. 7).
+    static __device__ __forceinline__ Raw drop(Raw r, int s)
     {
-        const f8_f32x4 a = *reinterpret_cast<const f8_f32x4_any *>(p), b = *reinterpret_cast<const f8_f32x4_any *>(p + 4);
+        float v[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = a[i];
-            v[4 + i] = b[i];
+        for (int i = 0; i < 8; ++i)
+            v[i] = r[i];
+#pragma unroll
+        for (int step = 4; step; step >>= 1)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = s & step ? (i + step < 8 ? v[i + step] : 0.0f) : v[i];
+        return {{v[0], v[1], v[2], v[3]}, {v[4], v[5], v[6], v[7]}};
+    }
+    // Elements at .. at+N-1 (N = 1, 2, 4) to p, unaligned.
+    template <int N> static __device__ __forceinline__ void put_part(float *p, const float *v)
+    {
+        typedef float VN __attribute__((ext_vector_type(N == 1 ? 2 : N)));
+        typedef VN VNany __attribute__((aligned(1)));
+        if constexpr (N == 1) {
+            *p = v[0];
+        } else {
+            VN o;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                o[i] = v[i];
+            *reinterpret_cast<VNany *>(p) = o;
         }
     }
     static __device__ __forceinline__ void store8(float *p, const float (&v)[8])
@@ -65,19 +83,41 @@ template <> struct Elt<float> {
         *reinterpret_cast<f8_f32x4_any *>(p) = f8_f32x4{v[0], v[1], v[2], v[3]};
         *reinterpret_cast<f8_f32x4_any *>(p + 4) = f8_f32x4{v[4], v[5], v[6], v[7]};
     }
-    static __device__ __forceinline__ float get(const float *p) { return *p; }
-    static __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 };
-template <typename T, typename V8, typename V8any> struct Elt16 {
+template <typename T, typename V8> struct Elt16 {
     typedef V8 Raw;
+    typedef V8 V8any __attribute__((aligned(1)));  // (as a template argument it would lose the attribute)
     static __device__ __forceinline__ Raw raw8(const T *p) { return *reinterpret_cast<const V8any *>(p); }
     static __device__ __forceinline__ void set(Raw &r, int i, T v) { r[i] = v; }
-    static __device__ __forceinline__ void load8(const T *p, float (&v)[8])
+    static __device__ __forceinline__ Raw drop(Raw r, int s)
     {
-        const V8 a = *reinterpret_cast<const V8any *>(p);
+        f8_u32x4 d;
+        __builtin_memcpy(&d, &r, 16);
+        uint32_t v[4] = {d[0], d[1], d[2], d[3]};
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = (float)a[i];
+        for (int step = 2; step; step >>= 1)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = s & 2 * step ? (i + step < 4 ? v[i + step] : 0u) : v[i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            d[i] = s & 1 ? __builtin_amdgcn_alignbit(i < 3 ? v[i + 1] : 0u, v[i], 16) : v[i];
+        __builtin_memcpy(&r, &d, 16);
+        return r;
+    }
+    template <int N> static __device__ __forceinline__ void put_part(T *p, const float *v)
+    {
+        typedef T VN __attribute__((ext_vector_type(N == 1 ? 2 : N)));
+        typedef VN VNany __attribute__((aligned(1)));
+        if constexpr (N == 1) {
+            *p = (T)v[0];
+        } else {
+            VN o;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                o[i] = (T)v[i];
+            *reinterpret_cast<VNany *>(p) = o;
+        }
     }
     static __device__ __forceinline__ void store8(T *p, const float (&v)[8])
     {
@@ -87,60 +127,90 @@ template <typename T, typename V8, typename V8any> struct Elt16 {
             a[i] = (T)v[i];
         *reinterpret_cast<V8any *>(p) = a;
     }
-    static __device__ __forceinline__ float get(const T *p) { return (float)*p; }
-    static __device__ __forceinline__ void put(T *p, float v) { *p = (T)v; }
 };
-template <> struct Elt<_Float16> : Elt16<_Float16, f8_h8, f8_h8_any> {};
-template <> struct Elt<__bf16> : Elt16<__bf16, f8_b8, f8_b8_any> {};
+template <> struct Elt<_Float16> : Elt16<_Float16, f8_h8> {};
+template <> struct Elt<__bf16> : Elt16<__bf16, f8_b8> {};
 
-// Elements c .. c+7 of a row of `cols`, zero past its end.
-template <typename T>
-__device__ __forceinline__ void row_load8(const T *row, int c, int cols, float (&v)[8])
-{
-    if (c + 8 <= cols) {
-        Elt<T>::load8(row + c, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = c + i < cols ? Elt<T>::get(row + c + i) : 0.0f;
-    }
-}
-// The same, unconverted (values requested ahead stay in as few registers as they have bytes).
+// Elements c .. c+7 of a row of `cols`, zero past its end, unconverted (values
+// requested ahead stay in as few registers as they have bytes).  The row's last
+// piece, where it is shorter, is read as the row's last 8 elements and shifted.
 template <typename T>
 __device__ __forceinline__ typename Elt<T>::Raw row_raw8(const T *row, int c, int cols)
 {
     if (c + 8 <= cols)
         return Elt<T>::raw8(row + c);
     typename Elt<T>::Raw r{};
+    if (c < cols) {
+        if (cols >= 8) {
+            r = Elt<T>::drop(Elt<T>::raw8(row + cols - 8), c + 8 - cols);
+        } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (c + i < cols)
-            Elt<T>::set(r, i, row[c + i]);
+            for (int i = 0; i < 7; ++i)
+                if (c + i < cols)
+                    Elt<T>::set(r, i, row[c + i]);
+        }
+    }
     return r;
 }
+template <typename T>
+__device__ __forceinline__ void row_load8(const T *row, int c, int cols, float (&v)[8])
+{
+    const typename Elt<T>::Raw r = row_raw8(row, c, cols);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = (float)r[i];
+}
+// A shorter last piece is written as 4, 2 and 1 elements, where its length has them.
 template <typename T>
 __device__ __forceinline__ void row_store8(T *row, int c, int cols, const float (&v)[8])
 {
     if (c + 8 <= cols) {
         Elt<T>::store8(row + c, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i < cols)
-                Elt<T>::put(row + c + i, v[i]);
+        return;
     }
+    const int n = cols - c;
+    if (n <= 0)
+        return;
+    T *p = row + c;
+    float u[4] = {v[0], v[1], v[2], v[3]};
+    if (n & 4) {
+        Elt<T>::template put_part<4>(p, v);
+        p += 4;
+        u[0] = v[4], u[1] = v[5], u[2] = v[6];
+    }
+    if (n & 2) {
+        Elt<T>::template put_part<2>(p, u);
+        p += 2;
+        u[0] = u[2];
+    }
+    if (n & 1)
+        Elt<T>::template put_part<1>(p, u);
 }
 // The same for 8 bytes held in two words.
 __device__ __forceinline__ void row_store8b(uint8_t *row, int c, int cols, uint32_t lo, uint32_t hi)
 {
+    typedef uint32_t u32_any __attribute__((aligned(1)));
+    typedef uint16_t u16_any __attribute__((aligned(1)));
     if (c + 8 <= cols) {
         *reinterpret_cast<f8_u32x2_any *>(row + c) = f8_u32x2{lo, hi};
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i < cols)
-                row[c + i] = (uint8_t)((i < 4 ? lo >> (8 * i) : hi >> (8 * (i - 4))) & 0xff);
+        return;
     }
+    const int n = cols - c;
+    if (n <= 0)
+        return;
+    uint8_t *p = row + c;
+    if (n & 4) {
+        *reinterpret_cast<u32_any *>(p) = lo;
+        p += 4;
+        lo = hi;
+    }
+    if (n & 2) {
+        *reinterpret_cast<u16_any *>(p) = (uint16_t)lo;
+        p += 2;
+        lo >>= 16;
+    }
+    if (n & 1)
+        *p = (uint8_t)lo;
 }
 
 // |x| as an unsigned number: ordered as |x| is, infinity above every finite

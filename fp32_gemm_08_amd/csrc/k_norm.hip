@@ -111,7 +111,7 @@ __global__ __launch_bounds__(NT) void rmsnorm_bwd_kernel(NormBwdArgs g)
     typedef typename Elt<T>::Raw Raw;
     constexpr int ROWS = NT / L;
     __shared__ float slot[2][NT / 64];
-    __shared__ float sums[ROWS > 1 ? NT * 8 : 1];
+    __shared__ float sums[ROWS > 1 ? NT * 8 * V : 1];
     const int lane = threadIdx.x % L, own = threadIdx.x / L;
     float dw[V][8], w[V][8];
 #pragma unroll
@@ -189,16 +189,17 @@ __global__ __launch_bounds__(NT) void rmsnorm_bwd_kernel(NormBwdArgs g)
         }
     } else {
         // the workgroup's rows of lanes, in order
-        static_assert(V == 1, "one piece a lane");
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            sums[(own * 8 + j) * L + lane] = dw[0][j];
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                sums[(own * 8 + j) * (V * L) + L * i + lane] = dw[i][j];
         __syncthreads();
         for (int c = threadIdx.x; c < g.cols; c += NT) {
             float s = 0.0f;
 #pragma unroll
             for (int r = 0; r < ROWS; ++r)
-                s += sums[(r * 8 + c % 8) * L + c / 8];
+                s += sums[(r * 8 + c % 8) * (V * L) + c / 8];
             out[c] = s;
         }
     }
@@ -246,7 +247,7 @@ void by_cols(int cols, F f)
     else if (cols <= 512)
         f.template run<T, 256, 64, 1>();
     else if (cols <= 1024)
-        f.template run<T, 128, 128, 1>();
+        f.template run<T, 256, 64, 2>();
     else if (cols <= 2048)
         f.template run<T, 256, 256, 1>();
     else if (cols <= 4096)

@@ -279,15 +279,17 @@ struct Bwd {
         rmsnorm_bwd_kernel<T, NT, L, V, AHEAD><<<(unsigned)a.groups, NT, 0, s>>>(a);
     }
 };
-// Workgroups of the backward pass: 8 wavefronts per CU (measured with 4 / 8 / 16
-// on rows of 4096 bf16: 122.6 / 105.5 / 114.8 us, of 1024: 166 / 106 / 112; of
-// few rows, one for each: 11.9 us on 1000 rows, 14.8 with 8 rows to a workgroup).
+// Workgroups of the backward pass: 12 wavefronts per CU, 8 of those that hold two
+// pieces a lane (measured in us with 512 / 768 / 1024 / 2048 workgroups of 256, bf16:
+// 65536 x 300 81 / 62 / 53 / 56, 65536 x 128 16.4 / 16.4 / 17.1 / 20.3, 32768 x 2048
+// 116 / 100 / 107 / 116; two pieces: 16384 x 4096 106 / 110 / 115 / 118).  Of few
+// rows, one row for each: 11.9 us on 1000 rows, 14.8 with 8 rows to a workgroup.
 struct Groups {
     int64_t rows;
     int64_t *out;
     template <typename T, int NT, int L, int V> void run()
     {
-        constexpr int64_t ROWS = NT / L, MOST = NT >= 512 ? 256 : 131072 / NT;
+        constexpr int64_t ROWS = NT / L, MOST = NT >= 512 ? 256 : V == 1 ? 768 : 512;
         *out = std::min((rows + ROWS - 1) / ROWS, MOST);
     }
 };

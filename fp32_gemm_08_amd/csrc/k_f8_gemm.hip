@@ -38,7 +38,7 @@ __device__ __forceinline__ void put8(const F8GemmArgs &g, int m, int n, const fl
         o[i] = g.alpha * v[i];
     if (g.beta != 0.0f) {
         float old[8];
-        row_load8(row, n, g.N, old);
+        row_load8<false>(row, n, g.N, old);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             o[i] = fmaf(g.beta, old[i], o[i]);

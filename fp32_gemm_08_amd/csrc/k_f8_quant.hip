@@ -39,7 +39,7 @@ __global__ __launch_bounds__(256) void f8_quantize_kernel(F8QuantArgs g)
     for (int i = 0; i < 8; ++i) {
         const int r = r0 + pr + i;
         if (r < g.rows && c < g.cols) {
-            row_load8(static_cast<const T *>(g.X) + (int64_t)r * g.ldx, c, g.cols, v[i]);
+            row_load8<true>(static_cast<const T *>(g.X) + (int64_t)r * g.ldx, c, g.cols, v[i]);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)

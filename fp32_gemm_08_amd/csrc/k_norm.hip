@@ -41,9 +41,9 @@ template <typename T>
 __device__ __forceinline__ void load_w8(const void *W, int w_f32, int c, int cols, float (&v)[8])
 {
     if (w_f32)
-        row_load8(static_cast<const float *>(W), c, cols, v);
+        row_load8<false>(static_cast<const float *>(W), c, cols, v);
     else
-        row_load8(static_cast<const T *>(W), c, cols, v);
+        row_load8<false>(static_cast<const T *>(W), c, cols, v);
 }
 
 template <typename T, int NT, int L, int V>
@@ -60,10 +60,10 @@ __global__ __launch_bounds__(NT) void rmsnorm_kernel(NormArgs g)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = 8 * (lane + L * i);
-        row_load8(x, c, g.cols, h[i]);
+        row_load8<true>(x, c, g.cols, h[i]);
         if (g.R) {
             float r[8];
-            row_load8(static_cast<const T *>(g.R) + row * g.ldr, c, g.cols, r);
+            row_load8<true>(static_cast<const T *>(g.R) + row * g.ldr, c, g.cols, r);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 h[i][j] += r[j];
@@ -127,10 +127,10 @@ __global__ __launch_bounds__(NT) void rmsnorm_bwd_kernel(NormBwdArgs g)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = 8 * (lane + L * i);
-            to_dy[i] = row_raw8(static_cast<const T *>(g.DY) + row * g.lddy, c, g.cols);
-            to_h[i] = row_raw8(static_cast<const T *>(g.H) + row * g.ldh, c, g.cols);
+            to_dy[i] = row_raw8<true>(static_cast<const T *>(g.DY) + row * g.lddy, c, g.cols);
+            to_h[i] = row_raw8<true>(static_cast<const T *>(g.H) + row * g.ldh, c, g.cols);
             if (g.DH)
-                to_dh[i] = row_raw8(static_cast<const T *>(g.DH) + row * g.lddh, c, g.cols);
+                to_dh[i] = row_raw8<true>(static_cast<const T *>(g.DH) + row * g.lddh, c, g.cols);
         }
     };
     const int64_t step = (int64_t)g.groups * ROWS;

@@ -146,7 +146,7 @@ int sgemm_f8_gemm(int format_a, int format_b, int b_block, int c_type, int64_t M
     const Operand outs[2] = {oc, ows}, ins[4] = {oa, ob, osa, osb};
     if (aliased(outs, ins, -1, 0))
         return SGEMM_ERR_ALIAS;
-    // the fast kernels' offsets within a tile of 256 rows are 32 bits wide
+    // the fast kernels' offsets within 8 rows are 32 bits wide
     const bool aligned = oa.rows_on(16) && ob.rows_on(16) && (M <= 1 || lda <= kMaxFastLd) && (N <= 1 || ldb <= kMaxFastLd) &&
                          (b_block == SGEMM_F8_ROW || N <= 128 || ldsb <= kMaxFastLd);
     F8GemmPlan p = f8_gemm_plan(b_block == SGEMM_F8_ROW, M, N, K, aligned);
@@ -164,8 +164,10 @@ int sgemm_f8_gemm(int format_a, int format_b, int b_block, int c_type, int64_t M
     a.SB = SB;
     a.C = C;
     a.ws = p.splits > 1 ? static_cast<float *>(workspace) : nullptr;
-    a.lda = lda;
-    a.ldb = ldb;
+    // the fast kernels take the rows past the last one to be out of range by their
+    // distance, which a single row may lack
+    a.lda = M > 1 ? lda : 256;
+    a.ldb = N > 1 ? ldb : 256;
     a.ldsa = ldsa;
     a.ldsb = ldsb;
     a.ldc = ldc;

@@ -66,6 +66,13 @@ __device__ __forceinline__ f8_f32x4 f8_mma(const Frag<FB, true> &b, const Frag<F
     return t;
 }
 
+// A quarter of them, added to t.
+template <int PART, int FA, int FB>
+__device__ __forceinline__ f8_f32x4 f8_mma_part(const Frag<FB, true> &b, const Frag<FA, true> &a, f8_f32x4 t)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.v[PART], a.v[PART], t, 0, 0, 0);
+}
+
 // 16 bytes of a row at any byte address, of which the first `valid` count (the
 // rest read as zero): whole aligned words, of which only those that hold a
 // counted byte are read, shifted into place.

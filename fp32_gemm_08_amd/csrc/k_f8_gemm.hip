@@ -236,6 +236,96 @@ __device__ __forceinline__ void f8_wait_barrier()
     asm volatile("s_barrier" ::: "memory");
 }
 
+// What a wavefront loads of each stage.
+template <class G, int S, bool ROWB>
+struct F8Stages {
+    typedef F8Pipe<G, S, ROWB> P;
+    uint8_t *smem;
+    // Operand rows: load j has the 8 rows from 8 * (w * LOADS + j) of the stage on,
+    // lane l row l/8, chunk (l % 8) ^ swizzle of that row.  The base of the 8 rows is
+    // uniform and the swizzle repeats every 16 rows, so the lane's offset is one of
+    // two.  Rows past the matrix and chunks past K deliver zeros by the range check
+    // (rows are 128 bytes or more apart, and 8 of them lie within 2^32 bytes: the
+    // caller's conditions).
+    const uint8_t *base[G::LOADS];
+    uint32_t bytes[G::LOADS];
+    uint32_t off[2];
+    bool past[2];                   // the lane's chunk is past K in the last stage
+    // This lane's scale: those of A's rows in the order (row % 16, row / 16) of a
+    // wavefront's rows, so that a lane reads its own together; those of B's
+    // columns in order, or of each fourth column.
+    const float *sbase;
+    int64_t sstep;
+    uint32_t soff, sblock;
+    int nk, tail;                   // stages, values of the last stage's rows
+
+    __device__ __forceinline__ F8Stages(const F8GemmArgs &g, uint8_t *lds, int m0, int n0, int w) : smem(lds)
+    {
+        const int lane = threadIdx.x & 63;
+        nk = (int)(((int64_t)g.K + 127) / 128);
+        tail = g.K - (nk - 1) * 128;
+#pragma unroll
+        for (int j = 0; j < G::LOADS; ++j) {
+            const int r = 8 * (w * G::LOADS + j);
+            const bool in_a = r < G::BM;
+            const int row = in_a ? m0 + r : n0 + r - G::BM, left = (in_a ? g.M : g.N) - row;
+            const int64_t ld = in_a ? g.lda : g.ldb;
+            base[j] = f8_pick(in_a, g.A, g.B) + (left > 0 ? row * ld : 0);
+            bytes[j] = left >= 8 ? F8_ALL : left > 0 ? (uint32_t)(left * ld) : 0;
+        }
+        // a wavefront's loads of both operands (LOADS of 6) would need two offsets each
+        static_assert(G::BM / 8 % G::LOADS == 0, "a wavefront's rows are of one operand");
+        const int64_t ld = 8 * w * G::LOADS < G::BM ? g.lda : g.ldb;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int c = (lane & 7) ^ f8_swz(8 * (w * G::LOADS + x) + lane / 8);
+            off[x] = (uint32_t)(lane / 8) * (uint32_t)ld + 16 * c;
+            past[x] = 16 * c >= tail;
+        }
+        sblock = w % P::NSC;
+        const int si = 64 * sblock + lane;
+        if (64 * (int)sblock < G::BM) {
+            sbase = g.SA + m0;
+            sstep = g.ldsa;
+            soff = 4u * (uint32_t)min(si / G::WM * G::WM + 16 * (si % G::FM) + si % G::WM / G::FM, g.M - 1 - m0);
+        } else if constexpr (ROWB) {
+            sbase = g.SB + n0;
+            sstep = g.ldsb;
+            soff = 4u * (uint32_t)min(si - G::BM, g.N - 1 - n0);
+        } else {
+            sbase = g.SB + (int64_t)(n0 / 128) * g.ldsb;
+            sstep = 1;
+            soff = 4u * (uint32_t)(min(n0 + 4 * (si - G::BM), g.N - 1) / 128 - n0 / 128) * (uint32_t)g.ldsb;
+        }
+    }
+    __device__ __forceinline__ uint8_t *stage(int kb) const { return smem + (kb % S) * P::STAGE; }
+    // Load j of stage kb (j = LOADS: its scales).  Stages past the last deliver
+    // zeros, so that every step makes the same loads.
+    __device__ __forceinline__ void fetch(int kb, int w, int j) const
+    {
+        if (j == G::LOADS)
+            f8_load_lds4(sbase + kb * sstep, kb < nk ? F8_ALL : 0, soff, stage(kb) + G::ROWS * 128 + 256 * sblock);
+        else
+            f8_load_lds16(base[j] + (int64_t)kb * 128, kb < nk ? bytes[j] : 0,
+                          kb == nk - 1 && past[j % 2] ? F8_PAST : off[j % 2], stage(kb) + (w * G::LOADS + j) * 1024);
+    }
+    // The bytes past K of the chunk that holds the last values of a row: zeros.
+    __device__ __forceinline__ void mask_tail() const
+    {
+        for (int r = threadIdx.x; r < G::ROWS; r += G::NT) {
+            f8_i32x4 *p = reinterpret_cast<f8_i32x4 *>(stage(nk - 1) + r * 128 + 16 * ((tail / 16) ^ f8_swz(r)));
+            *p = keep16(*p, tail % 16);
+        }
+        __syncthreads();
+    }
+};
+
+// Pipeline.  At the start of a step the fragments of the B rows and of the first A
+// rows are in registers.  Each row of blocks reads the next A rows under its
+// products.  The stage S-1 ahead is requested under the first rows, into the place
+// of the stage before this one.  In the last row every wavefront has read all of
+// this stage: there the wavefronts meet, and the next stage's fragments are read
+// under the last row's products.
 template <class G, int S, int FA, int FB, bool ROWB, bool EXACT>
 __global__ __launch_bounds__(G::NT) void f8_pipe_kernel(F8GemmArgs g)
 {
@@ -247,65 +337,7 @@ __global__ __launch_bounds__(G::NT) void f8_pipe_kernel(F8GemmArgs g)
     const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = w / G::WGN, wn = w % G::WGN;
-
-    // This lane's bytes in each of its wavefront's 1 KB blocks: row 8b + lane/8,
-    // chunk (lane % 8) ^ swizzle of that row; rows past the matrix repeat its
-    // last one.  Offsets from the tile's first row fit 32 bits (the caller's
-    // condition on the leading dimensions).
-    const uint8_t *base_a = g.A + (int64_t)m0 * g.lda, *base_b = g.B + (int64_t)n0 * g.ldb;
-    uint32_t off[G::LOADS];
-#pragma unroll
-    for (int j = 0; j < G::LOADS; ++j) {
-        const int b = w * G::LOADS + j, r = 8 * b + lane / 8;
-        const int rr = b < G::BM / 8 ? min(r, g.M - 1 - m0) : min(r - G::BM, g.N - 1 - n0);
-        off[j] = (uint32_t)rr * (uint32_t)(b < G::BM / 8 ? g.lda : g.ldb) + 16 * ((lane & 7) ^ f8_swz(r));
-    }
-    // This lane's scale: those of A's rows in the order (row % 16, row / 16) of a
-    // wavefront's rows, so that a lane reads its own together; those of B's
-    // columns in order, or of each fourth column.
-    const int sblock = w % P::NSC, si = 64 * sblock + lane;
-    const bool scale_a = 64 * sblock < G::BM;
-    const float *sbase;
-    int64_t sstep;
-    uint32_t soff;
-    if (scale_a) {
-        sbase = g.SA + m0;
-        sstep = g.ldsa;
-        soff = 4u * (uint32_t)min(si / G::WM * G::WM + 16 * (si % G::FM) + si % G::WM / G::FM, g.M - 1 - m0);
-    } else if constexpr (ROWB) {
-        sbase = g.SB + n0;
-        sstep = g.ldsb;
-        soff = 4u * (uint32_t)min(si - G::BM, g.N - 1 - n0);
-    } else {
-        sbase = g.SB + (int64_t)(n0 / 128) * g.ldsb;
-        sstep = 1;
-        soff = 4u * (uint32_t)(min(n0 + 4 * (si - G::BM), g.N - 1) / 128 - n0 / 128) * (uint32_t)g.ldsb;
-    }
-
-    const int nk = (int)(((int64_t)g.K + 127) / 128);
-    const int tail = g.K - (nk - 1) * 128;          // values of the last stage's rows
-    // Load j of stage kb (j = LOADS: its scales).  Chunks past K deliver zeros, and
-    // so do stages past the last, so that every step makes the same loads.
-    auto fetch = [&](int kb, int j) {
-        uint8_t *st = smem + (kb % S) * P::STAGE;
-        const uint32_t bytes = kb < nk ? F8_ALL : 0;
-        if (j == G::LOADS) {
-            f8_load_lds4(sbase + kb * sstep, bytes, soff, st + G::ROWS * 128 + 256 * sblock);
-            return;
-        }
-        const int b = w * G::LOADS + j, c = (lane & 7) ^ f8_swz(8 * b + lane / 8);
-        const uint32_t o = kb == nk - 1 && 16 * c >= tail ? F8_PAST : off[j];
-        f8_load_lds16(f8_pick(b < G::BM / 8, base_a, base_b) + (int64_t)kb * 128, bytes, o, st + b * 1024);
-    };
-    // The bytes past K of the chunk that holds the last values: zeros.
-    auto mask_tail = [&](int kb) {
-        for (int r = threadIdx.x; r < G::ROWS; r += G::NT) {
-            f8_i32x4 *p = reinterpret_cast<f8_i32x4 *>(smem + (kb % S) * P::STAGE + r * 128 +
-                                                       16 * ((tail / 16) ^ f8_swz(r)));
-            *p = keep16(*p, tail % 16);
-        }
-        __syncthreads();
-    };
+    const F8Stages<G, S, ROWB> in(g, smem, m0, n0, w);
 
     f8_f32x4 acc[G::FM][G::FN];
 #pragma unroll
@@ -323,92 +355,114 @@ __global__ __launch_bounds__(G::NT) void f8_pipe_kernel(F8GemmArgs g)
                        *reinterpret_cast<const f8_i32x4 *>(st + first + hi + i * 2048));
     };
 
-    // Pipeline.  At the start of a step the fragments of the B rows and of the
-    // first A rows are in registers.  Each row of blocks reads the next A rows
-    // under its products.  The stage S-1 ahead is requested under the first rows,
-    // into the place of the stage before this one.  In the last row every
-    // wavefront has read all of this stage: there the wavefronts meet, and the
-    // next stage's fragments are read under the last row's products.
     for (int st = 0; st < S - 1; ++st) {
-        poison_lds(smem + st * P::STAGE, P::STAGE);
+        poison_lds(in.stage(st), P::STAGE);
 #pragma unroll
         for (int j = 0; j <= G::LOADS; ++j)
-            fetch(st, j);
+            in.fetch(st, w, j);
     }
     f8_wait_barrier<(S - 2) * P::LOADS>();
-    if (nk == 1 && tail % 16)
-        mask_tail(0);
+    if (in.nk == 1 && in.tail % 16)
+        in.mask_tail();
     Frag<FB, EXACT> fb[G::FN];
-    f8_i32x8 ra[2];
 #pragma unroll
     for (int j = 0; j < G::FN; ++j)
         fb[j].set(read(smem, at_b, j));
+    f8_i32x8 ra[2];                              // the next rows of A
     ra[0] = read(smem, at_a, 0);
-    for (int kb = 0; kb < nk; ++kb) {
-        const uint8_t *st = smem + (kb % S) * P::STAGE, *next = smem + ((kb + 1) % S) * P::STAGE;
-        const float *sc = reinterpret_cast<const float *>(st + G::ROWS * 128);
-        poison_lds(smem + ((kb + S - 1) % S) * P::STAGE, P::STAGE);
-        float sa[G::FM], sb = 1.0f;
-        f8_f32x4 sbv[ROWB ? G::FN : 1];
+    for (int kb = 0; kb < in.nk; ++kb) {
+        const uint8_t *st = in.stage(kb), *next = in.stage(kb + 1);
+        const float *sca = reinterpret_cast<const float *>(st + G::ROWS * 128) + wm * G::WM + l16 * G::FM;
+        const float *scb = reinterpret_cast<const float *>(st + G::ROWS * 128) + G::BM +
+                           (ROWB ? wn * G::WN + 4 * q : wn * G::WN / 4);
+        poison_lds(in.stage(kb + S - 1), P::STAGE);
         // 16 x 16 block e = i * FN + j: its products while block e - LAG is scaled and
         // added (the wait for a product is then covered by the work between).  What the
         // next row needs is read right after a row's first product: the wait that comes
-        // before each row then finds reads that are a row old.
-        constexpr int NB = G::FM * G::FN, LAG = EXACT ? 2 : 3;
+        // before each row then finds reads that are a row old.  The bf16 form has no
+        // registers to spare: it reads the scales block by block, and converts the next
+        // B fragments one by one when the last row is done with them.
+        constexpr int NB = G::FM * G::FN, LAG = EXACT ? 1 : 3;
+        float sa[EXACT ? 2 : G::FM], sb = 1.0f;
+        f8_f32x4 sbv[EXACT ? 2 : ROWB ? G::FN : 1];
         f8_f32x4 t[LAG + 1];
         Frag<FA, EXACT> fa;
+        f8_i32x8 rb;
 #pragma unroll
         for (int e = 0; e < NB + LAG; ++e) {
             const int i = e / G::FN, j = e % G::FN;
             if (e < NB) {
                 if (j == 0)
-                    fa.set(ra[i & 1]);
-                t[e % (LAG + 1)] = f8_mma<FA, FB>(fb[j], fa);
+                    fa.set(ra[EXACT ? 0 : i & 1]);
+                f8_f32x4 &u = t[e % (LAG + 1)];
+                if constexpr (EXACT) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    u = f8_mma_part<0>(fb[j], fa, f8_f32x4{});
+                } else {
+                    u = f8_mma<FA, FB>(fb[j], fa);
+                }
                 __builtin_amdgcn_sched_barrier(0);
-                if (e == 0) {
+                if constexpr (EXACT) {
+                    if (j == 0)
+                        sa[i & 1] = sca[i];
+                    if (ROWB)
+                        sbv[e & 1] = *reinterpret_cast<const f8_f32x4 *>(scb + 16 * j);
+                    else if (e == 0)
+                        sb = scb[0];
+                } else if (e == 0) {
 #pragma unroll
                     for (int x = 0; x < G::FM; ++x)
-                        sa[x] = sc[wm * G::WM + l16 * G::FM + x];
+                        sa[x] = sca[x];
                     if constexpr (ROWB) {
 #pragma unroll
                         for (int x = 0; x < G::FN; ++x)
-                            sbv[x] = *reinterpret_cast<const f8_f32x4 *>(sc + G::BM + wn * G::WN + 16 * x + 4 * q);
+                            sbv[x] = *reinterpret_cast<const f8_f32x4 *>(scb + 16 * x);
                     } else {
-                        sb = sc[G::BM + wn * G::WN / 4];
+                        sb = scb[0];
                     }
                 }
                 if (j == 0 && i + 1 < G::FM)
-                    ra[(i + 1) & 1] = read(st, at_a, i + 1);
+                    ra[EXACT ? 0 : (i + 1) & 1] = read(st, at_a, i + 1);
                 if (e <= G::LOADS)
-                    fetch(kb + S - 1, e);
+                    in.fetch(kb + S - 1, w, e);
                 if (j == 0 && i + 1 == G::FM) {
                     f8_wait_barrier<(S - 2) * P::LOADS>();  // stage kb+1 has landed
-                    if (kb + 2 == nk && tail % 16)
-                        mask_tail(kb + 1);
+                    if (kb + 2 == in.nk && in.tail % 16)
+                        in.mask_tail();
+                    if (EXACT)
+                        rb = read(next, at_b, 0);
                     ra[0] = read(next, at_a, 0);
                 }
                 if (!EXACT && i + 1 == G::FM)
                     fb[j].set(read(next, at_b, j));
                 __builtin_amdgcn_sched_barrier(0);
+                if constexpr (EXACT) {
+                    u = f8_mma_part<1>(fb[j], fa, u);
+                    u = f8_mma_part<2>(fb[j], fa, u);
+                    u = f8_mma_part<3>(fb[j], fa, u);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
             if (e >= LAG) {
-                const int pi = (e - LAG) / G::FN, pj = (e - LAG) % G::FN;
-                const f8_f32x4 &u = t[(e - LAG) % (LAG + 1)];
+                const int pe = e - LAG, pi = pe / G::FN, pj = pe % G::FN;
+                const f8_f32x4 &u = t[pe % (LAG + 1)];
+                float &a = sa[EXACT ? pi & 1 : pi];
                 if (!ROWB && pj == 0)
-                    sa[pi] *= sb;
+                    a *= sb;
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                    acc[pi][pj][x] = fmaf(u[x], ROWB ? sa[pi] * sbv[ROWB ? pj : 0][x] : sa[pi], acc[pi][pj][x]);
+                    acc[pi][pj][x] = fmaf(u[x], ROWB ? a * sbv[EXACT ? pe & 1 : ROWB ? pj : 0][x] : a, acc[pi][pj][x]);
                 // the additions stay here: the compiler would sink them below the
                 // branch of the last row, and keep all products in registers till then
                 asm volatile("" : "+v"(acc[pi][pj]));
             }
             __builtin_amdgcn_sched_barrier(0);
-        }
-        if constexpr (EXACT) {
-#pragma unroll
-            for (int j = 0; j < G::FN; ++j)
-                fb[j].set(read(next, at_b, j));
+            if (EXACT && e < NB && i + 1 == G::FM) {
+                fb[j].set(rb);
+                if (j + 1 < G::FN)
+                    rb = read(next, at_b, j + 1);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
     }
     // the stages requested past the last one land before the LDS is used again

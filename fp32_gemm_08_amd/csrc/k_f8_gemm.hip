@@ -322,10 +322,11 @@ struct F8Stages {
 
 // Pipeline.  At the start of a step the fragments of the B rows and of the first A
 // rows are in registers.  Each row of blocks reads the next A rows under its
-// products.  The stage S-1 ahead is requested under the first rows, into the place
-// of the stage before this one.  In the last row every wavefront has read all of
-// this stage: there the wavefronts meet, and the next stage's fragments are read
-// under the last row's products.
+// products.  In the last row every wavefront has read all of this stage: there the
+// wavefronts meet, the stage S ahead is requested into its place, a load per
+// product (EARLY of them there and the others under the next step's first rows;
+// all of them under those 470 against 452 us at 8192^3, three per product 467), and
+// the next stage's fragments are read under the last row's products.
 template <class G, int S, int FA, int FB, bool ROWB, bool EXACT>
 __global__ __launch_bounds__(G::NT) void f8_pipe_kernel(F8GemmArgs g)
 {
@@ -362,6 +363,9 @@ __global__ __launch_bounds__(G::NT) void f8_pipe_kernel(F8GemmArgs g)
             in.fetch(st, w, j);
     }
     f8_wait_barrier<(S - 2) * P::LOADS>();
+#pragma unroll
+    for (int j = 0; j < G::FN - 1; ++j)
+        in.fetch(S - 1, w, j);
     if (in.nk == 1 && in.tail % 16)
         in.mask_tail();
     Frag<FB, EXACT> fb[G::FN];
@@ -382,7 +386,7 @@ __global__ __launch_bounds__(G::NT) void f8_pipe_kernel(F8GemmArgs g)
         // before each row then finds reads that are a row old.  The bf16 form has no
         // registers to spare: it reads the scales block by block, and converts the next
         // B fragments one by one when the last row is done with them.
-        constexpr int NB = G::FM * G::FN, LAG = EXACT ? 1 : 3;
+        constexpr int NB = G::FM * G::FN, LAG = EXACT ? 1 : 3, EARLY = G::FN - 1;
         float sa[EXACT ? 2 : G::FM], sb = 1.0f;
         f8_f32x4 sbv[EXACT ? 2 : ROWB ? G::FN : 1];
         f8_f32x4 t[LAG + 1];
@@ -423,8 +427,10 @@ __global__ __launch_bounds__(G::NT) void f8_pipe_kernel(F8GemmArgs g)
                 }
                 if (j == 0 && i + 1 < G::FM)
                     ra[EXACT ? 0 : (i + 1) & 1] = read(st, at_a, i + 1);
-                if (e <= G::LOADS)
-                    in.fetch(kb + S - 1, w, e);
+                if (EARLY + e <= G::LOADS)
+                    in.fetch(kb + S - 1, w, EARLY + e);
+                if (j > 0 && i + 1 == G::FM)
+                    in.fetch(kb + S, w, j - 1);
                 if (j == 0 && i + 1 == G::FM) {
                     f8_wait_barrier<(S - 2) * P::LOADS>();  // stage kb+1 has landed
                     if (kb + 2 == in.nk && in.tail % 16)

@@ -11,7 +11,7 @@ using namespace sgemm;
 namespace {
 
 constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1025;
-constexpr int64_t kMaxFastLd = int64_t{1} << 24;
+constexpr int64_t kMaxFastLd = int64_t{1} << 22;
 constexpr int64_t kMaxWorkItems = (int64_t{1} << 32) - 1;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -81,7 +81,7 @@ Operand scales(const float *p, int block, int64_t rows, int64_t cols, int64_t ld
 
 int finish(hipError_t e) { return e == hipSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH; }
 
-int threads_of(int kid) { return kid == KID_F8_S ? 256 : 1024; }
+int threads_of(int kid) { return kid == KID_F8_ANY ? 256 : 512; }
 
 }  // namespace
 
@@ -146,7 +146,8 @@ int sgemm_f8_gemm(int format_a, int format_b, int b_block, int c_type, int64_t M
     const Operand outs[2] = {oc, ows}, ins[4] = {oa, ob, osa, osb};
     if (aliased(outs, ins, -1, 0))
         return SGEMM_ERR_ALIAS;
-    // the fast kernels' offsets within 8 rows are 32 bits wide
+    // the fast kernels' offsets within a tile of 256 rows are 32 bits wide, beside those
+    // along K; they take the rows past the last one to be out of range by their distance
     const bool aligned = oa.rows_on(16) && ob.rows_on(16) && (M <= 1 || lda <= kMaxFastLd) && (N <= 1 || ldb <= kMaxFastLd) &&
                          (b_block == SGEMM_F8_ROW || N <= 128 || ldsb <= kMaxFastLd);
     F8GemmPlan p = f8_gemm_plan(b_block == SGEMM_F8_ROW, M, N, K, aligned);
@@ -164,10 +165,8 @@ int sgemm_f8_gemm(int format_a, int format_b, int b_block, int c_type, int64_t M
     a.SB = SB;
     a.C = C;
     a.ws = p.splits > 1 ? static_cast<float *>(workspace) : nullptr;
-    // the fast kernels take the rows past the last one to be out of range by their
-    // distance, which a single row may lack
-    a.lda = M > 1 ? lda : 256;
-    a.ldb = N > 1 ? ldb : 256;
+    a.lda = lda;
+    a.ldb = ldb;
     a.ldsa = ldsa;
     a.ldsb = ldsb;
     a.ldc = ldc;
@@ -179,7 +178,7 @@ int sgemm_f8_gemm(int format_a, int format_b, int b_block, int c_type, int64_t M
     a.beta = beta;
     a.c_type = c_type;
     (void)hipGetLastError();
-    return finish(launch_f8_gemm(a, p, format_a, format_b, b_block == SGEMM_F8_ROW, aligned,
+    return finish(launch_f8_gemm(a, p, format_a, format_b, b_block == SGEMM_F8_ROW,
                                  reinterpret_cast<hipStream_t>(stream)));
 }
 

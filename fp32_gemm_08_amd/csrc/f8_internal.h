@@ -12,10 +12,12 @@ constexpr float F8_FLOOR = 0x1p-90f;     // least block maximum: scales stay nor
 
 enum F8KernelId : int {
     KID_F8_NONE = 0,
-    KID_F8_SKINNY = 80,   // up to 64 rows of A: 16 columns of C per workgroup, k split over its wavefronts
-    KID_F8_S = 81,        // 64 x 64 tile
-    KID_F8_M = 82,        // 128 x 128 tile
-    KID_F8_L = 83,        // 256 x 256 tile
+    KID_F8_SKINNY = 80,   // up to 64 rows of A: 16 to 64 columns of C per workgroup, k split over its wavefronts
+    KID_F8_ANY = 81,      // rows at any alignment: 64 x 64 tile
+    KID_F8_S = 82,        // 64 x 64 tile
+    KID_F8_N = 83,        // 128 x 64 tile
+    KID_F8_M = 84,        // 128 x 128 tile
+    KID_F8_L = 85,        // 256 x 256 tile
 };
 
 struct F8GemmArgs {
@@ -33,11 +35,16 @@ struct F8GemmArgs {
 
 struct F8GemmPlan {
     int kid = KID_F8_NONE;
-    int64_t tiles_m = 0, tiles_n = 0, splits = 1, bytes = 0;
+    int64_t tiles_m = 0, tiles_n = 0, splits = 1, bytes = 0;    // bytes: of the workspace for the splits
 };
 F8GemmPlan f8_gemm_plan(bool row_b, int64_t M, int64_t N, int64_t K, bool aligned);
-hipError_t launch_f8_gemm(F8GemmArgs a, const F8GemmPlan &p, int format_a, int format_b, bool row_b, bool aligned,
-                          hipStream_t s);
+hipError_t launch_f8_gemm(F8GemmArgs a, const F8GemmPlan &p, int format_a, int format_b, bool row_b, hipStream_t s);
+// The tiles of aligned operands, a.kb_split k-blocks to each of `splits` (with
+// several, their partial sums go to a.ws).
+hipError_t launch_f8_small(const F8GemmArgs &a, int splits, int format_a, int format_b, bool row_b, hipStream_t s);
+hipError_t launch_f8_narrow(const F8GemmArgs &a, int splits, int format_a, int format_b, bool row_b, hipStream_t s);
+hipError_t launch_f8_medium(const F8GemmArgs &a, int splits, int format_a, int format_b, bool row_b, hipStream_t s);
+hipError_t launch_f8_large(const F8GemmArgs &a, int splits, int format_a, int format_b, bool row_b, hipStream_t s);
 // M <= 64, aligned operands: columns per workgroup, and the launch.
 int f8_skinny_cols(bool row_b, int64_t N);
 hipError_t launch_f8_skinny(const F8GemmArgs &a, int format_a, int format_b, bool row_b, hipStream_t s);

@@ -33,6 +33,7 @@ __device__ __forceinline__ uint32_t f8_pack4(float a, float b, float c, float d)
 // Vectors at any address: the hardware's global loads and stores of up to 16
 // bytes take every byte alignment, so rows that start anywhere are accessed whole.
 typedef f8_f32x4 f8_f32x4_any __attribute__((aligned(1)));
+typedef f8_i32x4 f8_i32x4_any __attribute__((aligned(1)));
 typedef _Float16 f8_h8 __attribute__((ext_vector_type(8)));
 typedef __bf16 f8_b8 __attribute__((ext_vector_type(8)));
 

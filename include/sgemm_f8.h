@@ -54,7 +54,7 @@ typedef enum { SGEMM_TYPE_F32 = 0, SGEMM_TYPE_FP16 = 1, SGEMM_TYPE_BF16 = 2 } sg
  * K == 0: C <- beta * C and A, B and their scales are not read.
  *
  * A, lda, B and ldb may have any alignment; bases and leading dimensions that
- * are multiples of 16 (and at most 2^24) run on the fast kernels (whole 16-byte
+ * are multiples of 16 (and at most 2^22) run on the fast kernels (whole 16-byte
  * loads), others on kernels that assemble their operands from aligned words.  On the fast
  * kernels the 16 bytes holding the last values of a row are read whole, the
  * bytes past K being ignored.
@@ -79,7 +79,7 @@ int sgemm_f8_gemm(int format_a, int format_b, int b_block, int c_type, int64_t M
 /* Host-only planning query: the kernel (0: nothing or no product to compute),
  * its grid of output tiles, the k-splits it makes with a sufficient workspace
  * and that workspace's bytes (0: no use for one).  `aligned`: whether A, lda, B
- * and ldb are all multiples of 16 and lda and ldb at most 2^24.  Output pointers may be NULL. */
+ * and ldb are all multiples of 16 and lda and ldb at most 2^22.  Output pointers may be NULL. */
 int sgemm_f8_gemm_plan(int b_block, int64_t M, int64_t N, int64_t K, int aligned, int *kernel_id,
                        int64_t *tiles_m, int64_t *tiles_n, int64_t *splits, int64_t *workspace_bytes);
 

@@ -19,5 +19,5 @@ from .sgemm import (ALGO, EXPORTS, LIB_PATH, PRECISION, SCRATCH_BYTES, SGEMM_ERR
                     sgemm_f32_transpose, sgemm_f32_transpose_algo, sgemm_f32_transpose_plan,
                     sgemm_f32_version, transpose)
 from .f8 import (F8_BLOCK, F8_EXPORTS, F8_FORMAT, RMSNORM_MAX_COLS, TYPE, f8_gemm, f8_quantize, rmsnorm,  # noqa: F401
-                 rmsnorm_backward, sgemm_f8_gemm, sgemm_f8_gemm_plan, sgemm_f8_quantize, sgemm_f8_rmsnorm,
+                 rmsnorm_backward, sgemm_f8_gemm, sgemm_f8_gemm_plan, sgemm_f8_gemm_workspace, sgemm_f8_quantize, sgemm_f8_rmsnorm,
                  sgemm_f8_rmsnorm_bwd, sgemm_f8_rmsnorm_bwd_plan)

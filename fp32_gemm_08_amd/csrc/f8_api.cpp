@@ -11,6 +11,7 @@ using namespace sgemm;
 namespace {
 
 constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1025;
+constexpr int64_t kAnyRoom = std::numeric_limits<int64_t>::max();
 constexpr int64_t kMaxFastLd = int64_t{1} << 22;
 constexpr int64_t kMaxWorkItems = (int64_t{1} << 32) - 1;
 
@@ -94,7 +95,7 @@ int sgemm_f8_gemm_plan(int b_block, int64_t M, int64_t N, int64_t K, int aligned
         return SGEMM_ERR_INVALID_VALUE;
     F8GemmPlan p;
     if (M > 0 && N > 0 && K > 0) {
-        p = f8_gemm_plan(b_block == SGEMM_F8_ROW, M, N, K, aligned == 1);
+        p = f8_gemm_plan(b_block == SGEMM_F8_ROW, M, N, K, aligned == 1, kAnyRoom, false);
         if (p.tiles_m * p.tiles_n * p.splits * threads_of(p.kid) > kMaxWorkItems)
             return SGEMM_ERR_INVALID_VALUE;
     }
@@ -108,6 +109,17 @@ int sgemm_f8_gemm_plan(int b_block, int64_t M, int64_t N, int64_t K, int aligned
         *splits = p.splits;
     if (workspace_bytes)
         *workspace_bytes = p.bytes;
+    return SGEMM_OK;
+}
+
+int sgemm_f8_gemm_workspace(int b_block, int64_t M, int64_t N, int64_t K, int aligned, int64_t *workspace_bytes)
+{
+    if (!known_block(b_block) || !dim_ok(M) || !dim_ok(N) || !dim_ok(K) || (aligned != 0 && aligned != 1))
+        return SGEMM_ERR_INVALID_VALUE;
+    if (workspace_bytes)
+        *workspace_bytes = M > 0 && N > 0 && K > 0
+                               ? f8_gemm_plan(b_block == SGEMM_F8_ROW, M, N, K, aligned == 1, kAnyRoom, true).bytes
+                               : 0;
     return SGEMM_OK;
 }
 
@@ -150,11 +162,9 @@ int sgemm_f8_gemm(int format_a, int format_b, int b_block, int c_type, int64_t M
     // along K; they take the rows past the last one to be out of range by their distance
     const bool aligned = oa.rows_on(16) && ob.rows_on(16) && (M <= 1 || lda <= kMaxFastLd) && (N <= 1 || ldb <= kMaxFastLd) &&
                          (b_block == SGEMM_F8_ROW || N <= 128 || ldsb <= kMaxFastLd);
-    F8GemmPlan p = f8_gemm_plan(b_block == SGEMM_F8_ROW, M, N, K, aligned);
+    const F8GemmPlan p = f8_gemm_plan(b_block == SGEMM_F8_ROW, M, N, K, aligned, workspace ? workspace_bytes : 0, true);
     if (p.tiles_m * p.tiles_n * p.splits * threads_of(p.kid) > kMaxWorkItems)
         return SGEMM_ERR_INVALID_VALUE;
-    if (workspace == nullptr || workspace_bytes < p.bytes)
-        p.splits = 1;
     const int dev = sgemm_f32_device_status();
     if (dev != SGEMM_OK)
         return dev;
@@ -164,7 +174,7 @@ int sgemm_f8_gemm(int format_a, int format_b, int b_block, int c_type, int64_t M
     a.SA = SA;
     a.SB = SB;
     a.C = C;
-    a.ws = p.splits > 1 ? static_cast<float *>(workspace) : nullptr;
+    a.ws = static_cast<float *>(workspace);
     a.lda = lda;
     a.ldb = ldb;
     a.ldsa = ldsa;

@@ -24,7 +24,7 @@ struct F8GemmArgs {
     const uint8_t *A, *B;
     const float *SA, *SB;
     void *C;
-    float *ws;                            // partial sums [split][M][N]; NULL: unsplit
+    float *ws;                            // the workspace; in a tile's kernel: partial sums [split][M][N], NULL: unsplit
     int64_t lda, ldb, ldsa, ldsb, ldc;
     int M, N, K;
     int tiles_m, tiles_n;                 // output tiles
@@ -35,9 +35,12 @@ struct F8GemmArgs {
 
 struct F8GemmPlan {
     int kid = KID_F8_NONE;
-    int64_t tiles_m = 0, tiles_n = 0, splits = 1, bytes = 0;    // bytes: of the workspace for the splits
+    int64_t tiles_m = 0, tiles_n = 0, splits = 1;
+    int64_t bytes = 0;      // of the workspace that it takes
+    int64_t pack = 0;       // of them, its first, for operands laid out anew
 };
-F8GemmPlan f8_gemm_plan(bool row_b, int64_t M, int64_t N, int64_t K, bool aligned);
+// The plan for a workspace of `room` bytes; may_pack: operands may be laid out anew there.
+F8GemmPlan f8_gemm_plan(bool row_b, int64_t M, int64_t N, int64_t K, bool aligned, int64_t room, bool may_pack);
 hipError_t launch_f8_gemm(F8GemmArgs a, const F8GemmPlan &p, int format_a, int format_b, bool row_b, hipStream_t s);
 // The tiles of aligned operands, a.kb_split k-blocks to each of `splits` (with
 // several, their partial sums go to a.ws).
@@ -45,7 +48,7 @@ hipError_t launch_f8_small(const F8GemmArgs &a, int splits, int format_a, int fo
 hipError_t launch_f8_narrow(const F8GemmArgs &a, int splits, int format_a, int format_b, bool row_b, hipStream_t s);
 hipError_t launch_f8_medium(const F8GemmArgs &a, int splits, int format_a, int format_b, bool row_b, hipStream_t s);
 hipError_t launch_f8_large(const F8GemmArgs &a, int splits, int format_a, int format_b, bool row_b, hipStream_t s);
-// M <= 64, aligned operands: columns per workgroup, and the launch.
+// Few rows of A: columns per workgroup, and the launch.
 int f8_skinny_cols(bool row_b, int64_t N);
 hipError_t launch_f8_skinny(const F8GemmArgs &a, int format_a, int format_b, bool row_b, hipStream_t s);
 // C <- beta * C for a rows x cols C of any type.

@@ -96,7 +96,7 @@ __device__ __forceinline__ f8_i32x4 load16_any(const uint8_t *p, int valid)
     return v;
 }
 
-// The same at a 16-byte aligned address: one load, masked.
+// The first `valid` bytes of 16, the others zero.
 __device__ __forceinline__ f8_i32x4 keep16(f8_i32x4 x, int valid)
 {
 #pragma unroll
@@ -106,13 +106,6 @@ __device__ __forceinline__ f8_i32x4 keep16(f8_i32x4 x, int valid)
     }
     return x;
 }
-__device__ __forceinline__ f8_i32x4 load16_aligned(const uint8_t *p, int valid)
-{
-    if (valid <= 0)
-        return f8_i32x4{};
-    return keep16(*reinterpret_cast<const f8_i32x4 *>(p), valid);
-}
-
 
 // Host side.  The variant of a kernel for a call's formats, B blocks, alignment and type
 // of C: f is called with the template arguments as integral constants.

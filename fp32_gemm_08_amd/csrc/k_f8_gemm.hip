@@ -163,7 +163,22 @@ __global__ __launch_bounds__(256) void f8_join_kernel(F8GemmArgs g, int splits)
     }
 }
 
+// The rows of A, then those of B, laid out with `ld` bytes a row, zeros past K.
+__global__ __launch_bounds__(256) void f8_pack_kernel(F8GemmArgs g, uint8_t *to, int64_t ld)
+{
+    const int64_t per_row = ld / 16, total = ((int64_t)g.M + g.N) * per_row;
+    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
+        const int64_t r = e / per_row, k = 16 * (e % per_row);
+        const uint8_t *p = (r < g.M ? g.A + r * g.lda : g.B + (r - g.M) * g.ldb) + k;
+        const int valid = (int)min<int64_t>(g.K - k, 16);
+        *reinterpret_cast<f8_i32x4 *>(to + r * ld + k) =
+            valid == 16 ? *reinterpret_cast<const f8_i32x4_any *>(p) : load16_any(p, valid);
+    }
+}
+int64_t f8_packed_ld(int64_t K) { return ceil_div(K, 128) * 128; }
+
 typedef F8Geo<64, 64, 2, 2> GS;
+constexpr int64_t kMaxPacked = int64_t{1} << 40;  // bytes of a packed operand
 constexpr int64_t kMaxJoin = int64_t{64} << 20;  // bytes of partial sums a call may ask for
 
 }  // namespace
@@ -176,39 +191,67 @@ constexpr int64_t kMaxJoin = int64_t{64} << 20;  // bytes of partial sums a call
 // 4096 x 4096 25.3; 256 x 256 4096 x 4096 x 1024 22.1, 4096^3 59.6; joining 2 MB 3.5,
 // 16 MB 10.5.  Of 28 shapes from 65 x 1024 x 1024 to 8192 x 8192 x 1024, timed with
 // every tile and 1, 2, 4 and 8 parts, the estimate takes the fastest or one within 5%.
-// (An FP32 C takes about twice the step with each tile.)
-F8GemmPlan f8_gemm_plan(bool row_b, int64_t M, int64_t N, int64_t K, bool aligned)
+// (An FP32 C takes about twice the step with each tile.)  `us` is the estimate.
+static F8GemmPlan plan_tiles(int64_t M, int64_t N, int64_t K, int64_t room, double &us)
+{
+    static const struct { int kid, bm, bn; double step, ends; } kTiles[4] = {{KID_F8_S, 64, 64, 0.36, 2.4},
+                                                                              {KID_F8_N, 128, 64, 0.45, 3.0},
+                                                                              {KID_F8_M, 128, 128, 0.6, 3.0},
+                                                                              {KID_F8_L, 256, 256, 1.6, 7.5}};
+    F8GemmPlan p;
+    const int64_t nk = ceil_div(K, F8_BLOCK);
+    for (const auto &t : kTiles) {
+        const int64_t tm = ceil_div(M, t.bm), tn = ceil_div(N, t.bn);
+        for (int64_t splits = 1; splits <= 16; splits *= 2) {
+            const int64_t part = ceil_div(nk, splits);
+            if (splits > 1 && (part < 4 || (splits - 1) * part >= nk || tm * tn * splits > 256 ||
+                               splits * M * N * 4 > std::min(room, kMaxJoin)))
+                break;
+            const int64_t bytes = splits > 1 ? splits * M * N * 4 : 0;
+            const double e = 2.0 + (double)ceil_div(tm * tn * splits, 256) * ((double)part * t.step + t.ends) +
+                             (splits > 1 ? 2.5 + (double)bytes * 0.5e-6 : 0.0);
+            if (p.kid == KID_F8_NONE || e < us) {
+                us = e;
+                p = F8GemmPlan{t.kid, tm, tn, splits, bytes, 0};
+            }
+        }
+    }
+    return p;
+}
+
+// Operands at other alignments go through the registers of the 64 x 64 tile, or, where
+// that takes longer, are first laid out anew in the workspace with rows of whole lines.
+// Measured (bf16 C, packed rows), through registers / laid out first: 1000 x 1017 x 999
+// 10.9 / 12.8 us, 512 x 4096 x 4095 35.3 / 27.5, 2048 x 2048 x 2047 33.6 / 20.8, 4096 x
+// 4096 x 4095 212 / 75.
+F8GemmPlan f8_gemm_plan(bool row_b, int64_t M, int64_t N, int64_t K, bool aligned, int64_t room, bool may_pack)
 {
     F8GemmPlan p;
-    if (!aligned || (M > 64 && N == 1)) {  // (a single row of B has no distance to the next)
-        p.kid = KID_F8_ANY;
-        p.tiles_m = ceil_div(M, GS::BM);
-        p.tiles_n = ceil_div(N, GS::BN);
-        return p;
-    }
-    if (M <= 64) {
+    double us = 0.0;
+    // few rows of A; of operands at other alignments up to 16 (N = K = 4096, through the
+    // wavefronts' registers / through the 64 x 64 tile: 1 row 11.3 / 17.3 us, 16 rows
+    // 17.6 / 17.7, 32 rows 25.0 / 18.0)
+    if (M <= (aligned ? 64 : 16)) {
         p.kid = KID_F8_SKINNY;
         p.tiles_m = 1;
         p.tiles_n = ceil_div(N, f8_skinny_cols(row_b, N));
         return p;
     }
-    static const struct { int kid, bm, bn; double step, ends; } kTiles[4] = {{KID_F8_S, 64, 64, 0.36, 2.4},
-                                                                              {KID_F8_N, 128, 64, 0.45, 3.0},
-                                                                              {KID_F8_M, 128, 128, 0.6, 3.0},
-                                                                              {KID_F8_L, 256, 256, 1.6, 7.5}};
-    const int64_t nk = ceil_div(K, F8_BLOCK);
-    double least = 0.0;
-    for (const auto &t : kTiles) {
-        const int64_t tm = ceil_div(M, t.bm), tn = ceil_div(N, t.bn);
-        for (int64_t splits = 1; splits <= 16; splits *= 2) {
-            const int64_t part = ceil_div(nk, splits), bytes = splits * M * N * 4;
-            if (splits > 1 && (part < 4 || (splits - 1) * part >= nk || tm * tn * splits > 256 || bytes > kMaxJoin))
-                break;
-            const double us = 2.0 + (double)ceil_div(tm * tn * splits, 256) * ((double)part * t.step + t.ends) +
-                              (splits > 1 ? 2.5 + (double)bytes * 0.5e-6 : 0.0);
-            if (p.kid == KID_F8_NONE || us < least) {
-                least = us;
-                p = F8GemmPlan{t.kid, tm, tn, splits, splits > 1 ? bytes : 0};
+    if (aligned && N > 1)  // (a single row of B has no distance to the next)
+        return plan_tiles(M, N, K, room, us);
+    p.kid = KID_F8_ANY;
+    p.tiles_m = ceil_div(M, GS::BM);
+    p.tiles_n = ceil_div(N, GS::BN);
+    if (may_pack && N > 1 && M <= kMaxPacked / f8_packed_ld(K) && N <= kMaxPacked / f8_packed_ld(K)) {
+        const int64_t pack = (M + N) * f8_packed_ld(K);
+        if (pack <= room) {
+            const F8GemmPlan q = plan_tiles(M, N, K, room - pack, us);
+            const double any = 3.0 + (double)ceil_div(K, F8_BLOCK) *
+                                         std::max(1.0, (double)p.tiles_m * (double)p.tiles_n * 1.7e-3);
+            if (us + 4.0 + (double)pack * 0.35e-6 < any) {
+                p = q;
+                p.bytes += pack;
+                p.pack = pack;
             }
         }
     }
@@ -219,6 +262,20 @@ hipError_t launch_f8_gemm(F8GemmArgs a, const F8GemmPlan &p, int format_a, int f
 {
     a.tiles_m = (int)p.tiles_m;
     a.tiles_n = (int)p.tiles_n;
+    if (p.pack) {
+        const int64_t ld = f8_packed_ld(a.K), chunks = ((int64_t)a.M + a.N) * (ld / 16);
+        uint8_t *to = reinterpret_cast<uint8_t *>(a.ws);
+        f8_pack_kernel<<<(unsigned)std::min<int64_t>(ceil_div(chunks, 256), 16384), 256, 0, s>>>(a, to, ld);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+        a.A = to;
+        a.B = to + (int64_t)a.M * ld;
+        a.lda = a.ldb = ld;
+        a.ws = reinterpret_cast<float *>(to + p.pack);
+    }
+    if (p.splits == 1)
+        a.ws = nullptr;
     const int nk = (int)ceil_div(a.K, F8_BLOCK), splits = (int)p.splits;
     a.kb_split = (nk + splits - 1) / splits;
     hipError_t e;

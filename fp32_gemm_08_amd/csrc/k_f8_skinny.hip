@@ -67,14 +67,14 @@ __global__ __launch_bounds__(512) void f8_skinny_kernel(F8GemmArgs g)
         if ((int64_t)kb * 128 + 128 <= g.K) {
 #pragma unroll
             for (int i = 0; i < NF; ++i)
-                b.x[i] = f8_join(*reinterpret_cast<const f8_i32x4 *>(row[i] + (int64_t)kb * 128),
-                                 *reinterpret_cast<const f8_i32x4 *>(row[i] + (int64_t)kb * 128 + 64));
+                b.x[i] = f8_join(*reinterpret_cast<const f8_i32x4_any *>(row[i] + (int64_t)kb * 128),
+                                 *reinterpret_cast<const f8_i32x4_any *>(row[i] + (int64_t)kb * 128 + 64));
         } else {
             const int valid = g.K - kb * 128 - 16 * q;
 #pragma unroll
             for (int i = 0; i < NF; ++i) {
                 const uint8_t *p = row[i] + (int64_t)kb * 128;
-                b.x[i] = f8_join(load16_aligned(p, valid), load16_aligned(p + 64, valid - 64));
+                b.x[i] = f8_join(load16_any(p, min(valid, 16)), load16_any(p + 64, min(valid - 64, 16)));
             }
         }
 #pragma unroll

@@ -20,8 +20,8 @@ TYPE = {"f32": 0, "fp16": 1, "bf16": 2}
 RMSNORM_MAX_COLS = 32768
 
 # Symbols declared in include/sgemm_f8.h.
-F8_EXPORTS = ("sgemm_f8_gemm", "sgemm_f8_gemm_plan", "sgemm_f8_quantize", "sgemm_f8_rmsnorm", "sgemm_f8_rmsnorm_bwd",
-              "sgemm_f8_rmsnorm_bwd_plan")
+F8_EXPORTS = ("sgemm_f8_gemm", "sgemm_f8_gemm_plan", "sgemm_f8_gemm_workspace", "sgemm_f8_quantize",
+              "sgemm_f8_rmsnorm", "sgemm_f8_rmsnorm_bwd", "sgemm_f8_rmsnorm_bwd_plan")
 
 _f8 = None
 
@@ -36,6 +36,7 @@ def _load_f8():
                 ("sgemm_f8_gemm", [ci, ci, ci, ci, i64, i64, i64, f32, vp, i64, vp, i64, vp, i64, vp, i64, f32, vp,
                                    i64, vp, i64, vp]),
                 ("sgemm_f8_gemm_plan", [ci, i64, i64, i64, ci, pi, pl, pl, pl, pl]),
+                ("sgemm_f8_gemm_workspace", [ci, i64, i64, i64, ci, pl]),
                 ("sgemm_f8_quantize", [ci, ci, ci, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp]),
                 ("sgemm_f8_rmsnorm", [ci, ci, i64, i64, vp, i64, vp, i64, vp, f32, vp, i64, vp, i64, vp, i64, vp, i64,
                                       vp, vp]),
@@ -62,6 +63,13 @@ def sgemm_f8_gemm_plan(b_block, M, N, K, aligned=1):
     st = _load_f8().sgemm_f8_gemm_plan(b_block, M, N, K, aligned, ctypes.byref(kid), ctypes.byref(tm),
                                        ctypes.byref(tn), ctypes.byref(sp), ctypes.byref(nb))
     return st, kid.value, tm.value, tn.value, sp.value, nb.value
+
+
+def sgemm_f8_gemm_workspace(b_block, M, N, K, aligned=1):
+    """Host-only query: (status, workspace_bytes) with which the product is fastest."""
+    nb = ctypes.c_int64(0)
+    st = _load_f8().sgemm_f8_gemm_workspace(b_block, M, N, K, aligned, ctypes.byref(nb))
+    return st, nb.value
 
 
 def sgemm_f8_quantize(block, format, x_type, rows, cols, X, ldx, Q, ldq, S, lds, QT=0, ldqt=0, ST=0, ldst=0,
@@ -195,8 +203,9 @@ def f8_gemm(A, SA, B, SB, C, alpha=1.0, beta=0.0, b_scale="tile", workspace=None
     (ceil(K/128), M) holds A's scales, one per 128 values of a row; SB holds
     B's: (ceil(N/128), ceil(K/128)) with ``b_scale`` "tile" (weights), or
     (ceil(K/128), N) with "row".  ``workspace``: a contiguous device tensor lent
-    for partial sums where few output tiles make it worthwhile
-    (sgemm_f8_gemm_plan says how much is used).
+    for partial sums where there are few output tiles, and for operands whose rows
+    do not start on 16-byte boundaries (sgemm_f8_gemm_workspace says how many
+    bytes serve; the call takes the fastest way that fits).
     """
     dev = _device(C)
     block = F8_BLOCK[b_scale]

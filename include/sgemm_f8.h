@@ -53,17 +53,18 @@ typedef enum { SGEMM_TYPE_F32 = 0, SGEMM_TYPE_FP16 = 1, SGEMM_TYPE_BF16 = 2 } sg
  * beta == 0: C is not read.  alpha == 0 or
  * K == 0: C <- beta * C and A, B and their scales are not read.
  *
- * A, lda, B and ldb may have any alignment; bases and leading dimensions that
- * are multiples of 16 (and at most 2^22) run on the fast kernels (whole 16-byte
- * loads), others on kernels that assemble their operands from aligned words.  On the fast
- * kernels the 16 bytes holding the last values of a row are read whole, the
- * bytes past K being ignored.
+ * A, lda, B and ldb may have any alignment.  Bases and leading dimensions that
+ * are multiples of 16 (and at most 2^22) run on the fast kernels, which read the
+ * 16 bytes holding the last values of a row whole and ignore those past K;
+ * others are assembled in registers, or first laid out anew in the workspace.
  *
  * workspace (NULL or 16-byte aligned, workspace_bytes long, overlapping no
  * operand): where too few output tiles exist to fill the GPU, k is split over
- * workgroups whose partial sums go there and are added in a fixed order;
- * with a smaller workspace than sgemm_f8_gemm_plan reports, or none, the call
- * runs unsplit.  Results are the same from call to call.
+ * workgroups whose partial sums go there and are added in a fixed order; and
+ * operands at other alignments are laid out there where that is faster.
+ * sgemm_f8_gemm_workspace says how many bytes serve; with fewer, or none, the
+ * call takes the fastest way that fits.  Results are the same from call to call
+ * with the same workspace size.
  *
  * SGEMM_ERR_INVALID_VALUE: an unknown format, block or type; a dimension below
  * 0 or above 2^31 - 1025; a leading dimension below its row length; NULL or
@@ -78,10 +79,14 @@ int sgemm_f8_gemm(int format_a, int format_b, int b_block, int c_type, int64_t M
 
 /* Host-only planning query: the kernel (0: nothing or no product to compute),
  * its grid of output tiles, the k-splits it makes with a sufficient workspace
- * and that workspace's bytes (0: no use for one).  `aligned`: whether A, lda, B
- * and ldb are all multiples of 16 and lda and ldb at most 2^22.  Output pointers may be NULL. */
+ * and the bytes of their partial sums (0: unsplit), operands staying where they
+ * are.  `aligned`: whether A, lda, B and ldb are all multiples of 16 and lda and
+ * ldb at most 2^22.  Output pointers may be NULL. */
 int sgemm_f8_gemm_plan(int b_block, int64_t M, int64_t N, int64_t K, int aligned, int *kernel_id,
                        int64_t *tiles_m, int64_t *tiles_n, int64_t *splits, int64_t *workspace_bytes);
+
+/* Host-only query: the workspace with which sgemm_f8_gemm is fastest (0: none). */
+int sgemm_f8_gemm_workspace(int b_block, int64_t M, int64_t N, int64_t K, int aligned, int64_t *workspace_bytes);
 
 /*
  * Quantise X (rows x cols of x_type) to 8 bits, in one pass over X, in either

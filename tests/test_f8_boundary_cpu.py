@@ -194,3 +194,20 @@ def test_tensor_wrappers_refuse_host_tensors():
         lib.f8_gemm(x, x, x, x, x)
     with pytest.raises(TypeError):
         lib.rmsnorm_backward(x, x, w, w, x)
+
+
+def test_gemm_workspace_query():
+    for block in (0, 1):
+        for M, N, K in ((1, 1, 1), (64, 4096, 4096), (128, 512, 8000), (512, 4096, 4096), (8192, 8192, 8192),
+                        (1000, 1017, 999), (2048, 2048, 2047)):
+            parts = lib.sgemm_f8_gemm_plan(block, M, N, K, 1)[5]
+            assert lib.sgemm_f8_gemm_workspace(block, M, N, K, 1) == (OK, parts)
+            st, nb = lib.sgemm_f8_gemm_workspace(block, M, N, K, 0)
+            assert st == OK and (nb == 0 or nb >= (M + N) * K)
+    assert lib.sgemm_f8_gemm_workspace(1, 4096, 4096, 4095, 0)[1] >= 8192 * 4096
+    assert lib.sgemm_f8_gemm_workspace(1, 0, 5, 5) == (OK, 0) and lib.sgemm_f8_gemm_workspace(1, 5, 5, 0) == (OK, 0)
+    big = (1 << 31) - 1025
+    assert lib.sgemm_f8_gemm_workspace(1, big, big, big, 0)[0] == OK
+    assert lib.sgemm_f8_gemm_workspace(1, big + 1, 1, 1)[0] == INVALID
+    assert lib.sgemm_f8_gemm_workspace(2, 5, 5, 5)[0] == INVALID
+    assert lib.sgemm_f8_gemm_workspace(1, 5, 5, 5, 3)[0] == INVALID

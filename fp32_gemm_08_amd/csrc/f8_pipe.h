@@ -14,7 +14,10 @@ struct F8Pipe {
     static constexpr int S = S_;
     static constexpr int SCALES = G::BM + (ROWB ? G::BN : 64);  // floats of a stage
     static constexpr int NSC = SCALES / 64;                     // loads that fetch them
-    static constexpr int STAGE = G::ROWS * 128 + SCALES * 4;
+    static constexpr int STAGE = G::ROWS * 128;                 // bytes of a stage's rows
+    // A slot of scales more than stages: the bf16 form reads scales in a stage's last row,
+    // where the rows' place is given to the stage S ahead already.
+    static constexpr int BYTES = S * STAGE + (S + 1) * SCALES * 4;
     static constexpr int LOADS = G::LOADS + 1;                  // per wavefront and stage
     static_assert(NSC <= G::NW && SCALES % 64 == 0, "one scale load per wavefront fetches all");
     // a step's loads: EARLY under the last products of the step before, PER under each
@@ -22,7 +25,7 @@ struct F8Pipe {
     static constexpr int EARLY = G::FN - 1, FREE = (G::FM - 1) * G::FN;
     static constexpr int PER = (LOADS - EARLY + FREE - 1) / FREE;
     static_assert(EARLY <= LOADS, "fewer loads than places");
-    static_assert(S * STAGE <= 160 * 1024 && (S - 2) * LOADS <= 63, "LDS size, vmcnt range");
+    static_assert(BYTES <= 160 * 1024 && (S - 2) * LOADS <= 63, "LDS size, vmcnt range");
 };
 
 // Direct global -> LDS loads of 16 (or 4) bytes per lane from `base` + the lane's
@@ -130,12 +133,16 @@ struct F8Stages {
         sbase += first * sstep;
     }
     __device__ __forceinline__ uint8_t *stage(int kb) const { return smem + (kb % S) * P::STAGE; }
+    __device__ __forceinline__ uint8_t *scales(int kb) const
+    {
+        return smem + S * P::STAGE + (kb % (S + 1)) * (P::SCALES * 4);
+    }
     // Load j of stage kb (j = LOADS: its scales).  Stages past the last deliver
     // zeros, so that every step makes the same loads.
     __device__ __forceinline__ void fetch(int kb, int w, int j) const
     {
         if (j == G::LOADS)
-            f8_load_lds4(sbase + kb * sstep, kb < nk ? F8_ALL : 0, soff, stage(kb) + G::ROWS * 128 + 256 * sblock);
+            f8_load_lds4(sbase + kb * sstep, kb < nk ? F8_ALL : 0, soff, scales(kb) + 256 * sblock);
         else {
             const bool second = FEW && MIXED && 8 * (w * G::LOADS + j) >= G::BM;
             const int x = FEW ? 0 : j, y = BASES > 1 && FEW ? 1 : x;
@@ -168,7 +175,7 @@ template <class G, int S, int FA, int FB, bool ROWB, bool EXACT>
 __global__ __launch_bounds__(G::NT) void f8_pipe_kernel(F8GemmArgs g)
 {
     typedef F8Pipe<G, S, ROWB> P;
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[S * P::STAGE];
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[P::BYTES];
     int tm, tn;
     const int tiles = g.tiles_m * g.tiles_n, split = blockIdx.x / tiles;
     f8_map_tile(blockIdx.x % tiles, g.tiles_m, g.tiles_n, tm, tn);
@@ -194,7 +201,7 @@ __global__ __launch_bounds__(G::NT) void f8_pipe_kernel(F8GemmArgs g)
                        *reinterpret_cast<const f8_i32x4 *>(st + first + hi + i * 2048));
     };
 
-    poison_lds(smem, S * P::STAGE);
+    poison_lds(smem, P::BYTES);
     for (int st = 0; st < S - 1; ++st) {
 #pragma unroll
         for (int j = 0; j <= G::LOADS; ++j)
@@ -214,8 +221,8 @@ __global__ __launch_bounds__(G::NT) void f8_pipe_kernel(F8GemmArgs g)
     ra[0] = read(smem, at_a, 0);
     for (int kb = 0; kb < in.nk; ++kb) {
         const uint8_t *st = in.stage(kb), *next = in.stage(kb + 1);
-        const float *sca = reinterpret_cast<const float *>(st + G::ROWS * 128) + wm * G::WM + l16 * G::FM;
-        const float *scb = reinterpret_cast<const float *>(st + G::ROWS * 128) + G::BM +
+        const float *sca = reinterpret_cast<const float *>(in.scales(kb)) + wm * G::WM + l16 * G::FM;
+        const float *scb = reinterpret_cast<const float *>(in.scales(kb)) + G::BM +
                            (ROWB ? wn * G::WN + 4 * q : wn * G::WN / 4);
         // 16 x 16 block e = i * FN + j: its products while block e - LAG is scaled and
         // added (the wait for a product is then covered by the work between).  What the
@@ -331,7 +338,7 @@ __global__ __launch_bounds__(G::NT) void f8_flat_kernel(F8GemmArgs g)
 {
     typedef F8Pipe<G, S, ROWB> P;
     static_assert((S - 1) * P::LOADS <= 63, "vmcnt range");
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[S * P::STAGE];
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[P::BYTES];
     int tm, tn;
     const int tiles = g.tiles_m * g.tiles_n, split = blockIdx.x / tiles;
     f8_map_tile(blockIdx.x % tiles, g.tiles_m, g.tiles_n, tm, tn);
@@ -354,7 +361,8 @@ __global__ __launch_bounds__(G::NT) void f8_flat_kernel(F8GemmArgs g)
         float sa[G::FM], sb;
         f8_f32x4 sbv[ROWB ? G::FN : 1];
     } set[2];
-    auto read = [&](Set &x, const uint8_t *st) {
+    auto read = [&](Set &x, int kb) {
+        const uint8_t *st = in.stage(kb);
         const uint8_t *a = st + wm * G::WM * 128, *b = st + (G::BM + wn * G::WN) * 128;
 #pragma unroll
         for (int j = 0; j < G::FN; ++j)
@@ -364,7 +372,7 @@ __global__ __launch_bounds__(G::NT) void f8_flat_kernel(F8GemmArgs g)
         for (int i = 0; i < G::FM; ++i)
             x.a[i] = f8_join(*reinterpret_cast<const f8_i32x4 *>(a + lo + i * 2048),
                              *reinterpret_cast<const f8_i32x4 *>(a + hi + i * 2048));
-        const float *sc = reinterpret_cast<const float *>(st + G::ROWS * 128);
+        const float *sc = reinterpret_cast<const float *>(in.scales(kb));
 #pragma unroll
         for (int i = 0; i < G::FM; ++i)
             x.sa[i] = sc[wm * G::WM + l16 * G::FM + i];
@@ -381,7 +389,7 @@ __global__ __launch_bounds__(G::NT) void f8_flat_kernel(F8GemmArgs g)
         poison_lds(in.stage(kb), P::STAGE);
         if (kb + 2 == in.nk && in.tail % 16)
             in.mask_tail();
-        read(next, in.stage(kb + 1));
+        read(next, kb + 1);
         __builtin_amdgcn_sched_barrier(0);
         Frag<FB, EXACT> fb[G::FN];
         Frag<FA, EXACT> fa;
@@ -414,7 +422,7 @@ __global__ __launch_bounds__(G::NT) void f8_flat_kernel(F8GemmArgs g)
         }
     };
 
-    poison_lds(smem, S * P::STAGE);
+    poison_lds(smem, P::BYTES);
     for (int st = 0; st < S; ++st)
 #pragma unroll
         for (int j = 0; j <= G::LOADS; ++j)
@@ -422,7 +430,7 @@ __global__ __launch_bounds__(G::NT) void f8_flat_kernel(F8GemmArgs g)
     f8_wait_barrier<(S - 1) * P::LOADS>();
     if (in.nk == 1 && in.tail % 16)
         in.mask_tail();
-    read(set[0], smem);
+    read(set[0], 0);
     for (int kb = 0; kb < in.nk; kb += 2) {
         step(set[0], set[1], kb);
         if (kb + 1 < in.nk)

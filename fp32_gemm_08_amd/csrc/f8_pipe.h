@@ -9,15 +9,16 @@ namespace {
 typedef __attribute__((address_space(3))) void f8_lds;
 
 // S stages rotate, filled by direct global -> LDS loads.
-template <class G, int S_, bool ROWB>
+template <class G, int S_, bool ROWB, bool LATE>
 struct F8Pipe {
     static constexpr int S = S_;
     static constexpr int SCALES = G::BM + (ROWB ? G::BN : 64);  // floats of a stage
     static constexpr int NSC = SCALES / 64;                     // loads that fetch them
     static constexpr int STAGE = G::ROWS * 128;                 // bytes of a stage's rows
-    // A slot of scales more than stages: the bf16 form reads scales in a stage's last row,
-    // where the rows' place is given to the stage S ahead already.
-    static constexpr int BYTES = S * STAGE + (S + 1) * SCALES * 4;
+    // LATE: scales are read in a stage's last row, where the place of the stage is given
+    // to the one S ahead already: they have twice the places.
+    static constexpr int SLOTS = LATE ? 2 * S : S;
+    static constexpr int BYTES = S * STAGE + SLOTS * SCALES * 4;
     static constexpr int LOADS = G::LOADS + 1;                  // per wavefront and stage
     static_assert(NSC <= G::NW && SCALES % 64 == 0, "one scale load per wavefront fetches all");
     // a step's loads: EARLY under the last products of the step before, PER under each
@@ -60,9 +61,9 @@ __device__ __forceinline__ void f8_wait_barrier()
 }
 
 // What a wavefront loads of each stage.
-template <class G, int S, bool ROWB>
+template <class G, int S, bool ROWB, bool LATE>
 struct F8Stages {
-    typedef F8Pipe<G, S, ROWB> P;
+    typedef F8Pipe<G, S, ROWB, LATE> P;
     uint8_t *smem;
     // Operand rows: load j has the 8 rows from 8 * (w * LOADS + j) of the stage on,
     // lane l row l/8, chunk (l % 8) ^ swizzle of that row (which repeats every 16 rows).
@@ -135,7 +136,7 @@ struct F8Stages {
     __device__ __forceinline__ uint8_t *stage(int kb) const { return smem + (kb % S) * P::STAGE; }
     __device__ __forceinline__ uint8_t *scales(int kb) const
     {
-        return smem + S * P::STAGE + (kb % (S + 1)) * (P::SCALES * 4);
+        return smem + S * P::STAGE + (kb % P::SLOTS) * (P::SCALES * 4);
     }
     // Load j of stage kb (j = LOADS: its scales).  Stages past the last deliver
     // zeros, so that every step makes the same loads.
@@ -174,7 +175,7 @@ struct F8Stages {
 template <class G, int S, int FA, int FB, bool ROWB, bool EXACT>
 __global__ __launch_bounds__(G::NT) void f8_pipe_kernel(F8GemmArgs g)
 {
-    typedef F8Pipe<G, S, ROWB> P;
+    typedef F8Pipe<G, S, ROWB, EXACT> P;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[P::BYTES];
     int tm, tn;
     const int tiles = g.tiles_m * g.tiles_n, split = blockIdx.x / tiles;
@@ -183,7 +184,7 @@ __global__ __launch_bounds__(G::NT) void f8_pipe_kernel(F8GemmArgs g)
     const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = w / G::WGN, wn = w % G::WGN;
-    const F8Stages<G, S, ROWB> in(g, smem, m0, n0, w, split);
+    const F8Stages<G, S, ROWB, EXACT> in(g, smem, m0, n0, w, split);
 
     f8_f32x4 acc[G::FM][G::FN];
 #pragma unroll
@@ -336,7 +337,7 @@ __global__ __launch_bounds__(G::NT) void f8_pipe_kernel(F8GemmArgs g)
 template <class G, int S, int FA, int FB, bool ROWB, bool EXACT>
 __global__ __launch_bounds__(G::NT) void f8_flat_kernel(F8GemmArgs g)
 {
-    typedef F8Pipe<G, S, ROWB> P;
+    typedef F8Pipe<G, S, ROWB, false> P;
     static_assert((S - 1) * P::LOADS <= 63, "vmcnt range");
     __shared__ __attribute__((aligned(1024))) uint8_t smem[P::BYTES];
     int tm, tn;
@@ -346,7 +347,7 @@ __global__ __launch_bounds__(G::NT) void f8_flat_kernel(F8GemmArgs g)
     const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = w / G::WGN, wn = w % G::WGN;
-    const F8Stages<G, S, ROWB> in(g, smem, m0, n0, w, split);
+    const F8Stages<G, S, ROWB, false> in(g, smem, m0, n0, w, split);
 
     f8_f32x4 acc[G::FM][G::FN];
 #pragma unroll

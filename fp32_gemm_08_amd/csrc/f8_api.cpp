@@ -12,7 +12,6 @@ namespace {
 
 constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1025;
 constexpr int64_t kAnyRoom = std::numeric_limits<int64_t>::max();
-constexpr int64_t kMaxFastLd = int64_t{1} << 22;
 constexpr int64_t kMaxWorkItems = (int64_t{1} << 32) - 1;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -158,16 +157,6 @@ int sgemm_f8_gemm(int format_a, int format_b, int b_block, int c_type, int64_t M
     const Operand outs[2] = {oc, ows}, ins[4] = {oa, ob, osa, osb};
     if (aliased(outs, ins, -1, 0))
         return SGEMM_ERR_ALIAS;
-    // the fast kernels' offsets within a tile of 256 rows are 32 bits wide, beside those
-    // along K; they take the rows past the last one to be out of range by their distance
-    const bool aligned = oa.rows_on(16) && ob.rows_on(16) && (M <= 1 || lda <= kMaxFastLd) && (N <= 1 || ldb <= kMaxFastLd) &&
-                         (b_block == SGEMM_F8_ROW || N <= 128 || ldsb <= kMaxFastLd);
-    const F8GemmPlan p = f8_gemm_plan(b_block == SGEMM_F8_ROW, M, N, K, aligned, workspace ? workspace_bytes : 0, true);
-    if (p.tiles_m * p.tiles_n * p.splits * threads_of(p.kid) > kMaxWorkItems)
-        return SGEMM_ERR_INVALID_VALUE;
-    const int dev = sgemm_f32_device_status();
-    if (dev != SGEMM_OK)
-        return dev;
     F8GemmArgs a;
     a.A = static_cast<const uint8_t *>(A);
     a.B = static_cast<const uint8_t *>(B);
@@ -187,6 +176,13 @@ int sgemm_f8_gemm(int format_a, int format_b, int b_block, int c_type, int64_t M
     a.alpha = alpha;
     a.beta = beta;
     a.c_type = c_type;
+    const F8GemmPlan p = f8_call_plan(a, oa.rows_on(16) && ob.rows_on(16), b_block == SGEMM_F8_ROW,
+                                      workspace ? workspace_bytes : 0);
+    if (p.tiles_m * p.tiles_n * p.splits * threads_of(p.kid) > kMaxWorkItems)
+        return SGEMM_ERR_INVALID_VALUE;
+    const int dev = sgemm_f32_device_status();
+    if (dev != SGEMM_OK)
+        return dev;
     (void)hipGetLastError();
     return finish(launch_f8_gemm(a, p, format_a, format_b, b_block == SGEMM_F8_ROW,
                                  reinterpret_cast<hipStream_t>(stream)));

@@ -9,6 +9,10 @@ namespace sgemm {
 
 constexpr int F8_BLOCK = 128;            // values per scale
 constexpr float F8_FLOOR = 0x1p-90f;     // least block maximum: scales stay normal numbers
+// Largest leading dimension of the pipelined kernels' operands, and of the tile scales
+// they read across tiles: they hold a row's offset within a tile of 256 rows, the byte
+// count of a tile's last rows and the offset of a tile's second row of scales in 32 bits.
+constexpr int64_t F8_MAX_LD = int64_t{1} << 22;
 
 enum F8KernelId : int {
     KID_F8_NONE = 0,
@@ -39,8 +43,11 @@ struct F8GemmPlan {
     int64_t bytes = 0;      // of the workspace that it takes
     int64_t pack = 0;       // of them, its first, for operands laid out anew
 };
-// The plan for a workspace of `room` bytes; may_pack: operands may be laid out anew there.
+// The plan for a workspace of `room` bytes.  aligned: the pipelined kernels can take the
+// operands where they are; may_pack: operands may be laid out anew in the workspace.
 F8GemmPlan f8_gemm_plan(bool row_b, int64_t M, int64_t N, int64_t K, bool aligned, int64_t room, bool may_pack);
+// The plan of a call; rows_on_16: the rows of A and of B start on 16-byte boundaries.
+F8GemmPlan f8_call_plan(const F8GemmArgs &a, bool rows_on_16, bool row_b, int64_t room);
 hipError_t launch_f8_gemm(F8GemmArgs a, const F8GemmPlan &p, int format_a, int format_b, bool row_b, hipStream_t s);
 // The tiles of aligned operands, a.kb_split k-blocks to each of `splits` (with
 // several, their partial sums go to a.ws).

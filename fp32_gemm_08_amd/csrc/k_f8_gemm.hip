@@ -228,6 +228,7 @@ F8GemmPlan f8_gemm_plan(bool row_b, int64_t M, int64_t N, int64_t K, bool aligne
 {
     F8GemmPlan p;
     double us = 0.0;
+    aligned = aligned && K <= F8_MAX_LD;  // (rows that do not overlap lie at least K apart)
     // few rows of A; of operands at other alignments up to 16 (N = K = 4096, through the
     // wavefronts' registers / through the 64 x 64 tile: 1 row 11.3 / 17.3 us, 16 rows
     // 17.6 / 17.7, 32 rows 25.0 / 18.0)
@@ -242,7 +243,7 @@ F8GemmPlan f8_gemm_plan(bool row_b, int64_t M, int64_t N, int64_t K, bool aligne
     p.kid = KID_F8_ANY;
     p.tiles_m = ceil_div(M, GS::BM);
     p.tiles_n = ceil_div(N, GS::BN);
-    if (may_pack && N > 1 && M <= kMaxPacked / f8_packed_ld(K) && N <= kMaxPacked / f8_packed_ld(K)) {
+    if (may_pack && N > 1 && f8_packed_ld(K) <= F8_MAX_LD && M <= kMaxPacked / f8_packed_ld(K) && N <= kMaxPacked / f8_packed_ld(K)) {
         const int64_t pack = (M + N) * f8_packed_ld(K);
         if (pack <= room) {
             const F8GemmPlan q = plan_tiles(M, N, K, room - pack, us);
@@ -258,10 +259,29 @@ F8GemmPlan f8_gemm_plan(bool row_b, int64_t M, int64_t N, int64_t K, bool aligne
     return p;
 }
 
+// Whether the tile scales of B lie near enough for the pipelined kernels (a tile of up to
+// 128 columns reads one row of them).
+static bool f8_scales_near(const F8GemmArgs &a, bool row_b)
+{
+    return row_b || a.N <= 128 || a.ldsb <= F8_MAX_LD;
+}
+
+F8GemmPlan f8_call_plan(const F8GemmArgs &a, bool rows_on_16, bool row_b, int64_t room)
+{
+    const bool near = f8_scales_near(a, row_b);
+    const bool aligned = rows_on_16 && near && (a.M <= 1 || a.lda <= F8_MAX_LD) && (a.N <= 1 || a.ldb <= F8_MAX_LD);
+    return f8_gemm_plan(row_b, a.M, a.N, a.K, aligned, room, near);
+}
+
 hipError_t launch_f8_gemm(F8GemmArgs a, const F8GemmPlan &p, int format_a, int format_b, bool row_b, hipStream_t s)
 {
     a.tiles_m = (int)p.tiles_m;
     a.tiles_n = (int)p.tiles_n;
+    if (p.kid >= KID_F8_S) {  // what the pipelined kernels' 32-bit offsets need
+        const int64_t ld = p.pack ? f8_packed_ld(a.K) : std::max(a.lda, a.ldb);
+        if (ld > F8_MAX_LD || !f8_scales_near(a, row_b))
+            return hipErrorInvalidValue;
+    }
     if (p.pack) {
         const int64_t ld = f8_packed_ld(a.K), chunks = ((int64_t)a.M + a.N) * (ld / 16);
         uint8_t *to = reinterpret_cast<uint8_t *>(a.ws);

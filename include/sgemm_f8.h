@@ -56,7 +56,9 @@ typedef enum { SGEMM_TYPE_F32 = 0, SGEMM_TYPE_FP16 = 1, SGEMM_TYPE_BF16 = 2 } sg
  * A, lda, B and ldb may have any alignment.  Bases and leading dimensions that
  * are multiples of 16 (and at most 2^22) run on the fast kernels, which read the
  * 16 bytes holding the last values of a row whole and ignore those past K;
- * others are assembled in registers, or first laid out anew in the workspace.
+ * others are assembled in registers, or (K up to 2^22) first laid out anew in the
+ * workspace.  Tile scales with ldsb above 2^22 and N above 128 keep a call off the
+ * fast kernels.
  *
  * workspace (NULL or 16-byte aligned, workspace_bytes long, overlapping no
  * operand): where too few output tiles exist to fill the GPU, k is split over
@@ -81,7 +83,7 @@ int sgemm_f8_gemm(int format_a, int format_b, int b_block, int c_type, int64_t M
  * its grid of output tiles, the k-splits it makes with a sufficient workspace
  * and the bytes of their partial sums (0: unsplit), operands staying where they
  * are.  `aligned`: whether A, lda, B and ldb are all multiples of 16 and lda and
- * ldb at most 2^22.  Output pointers may be NULL. */
+ * ldb (so K too) at most 2^22.  Output pointers may be NULL. */
 int sgemm_f8_gemm_plan(int b_block, int64_t M, int64_t N, int64_t K, int aligned, int *kernel_id,
                        int64_t *tiles_m, int64_t *tiles_n, int64_t *splits, int64_t *workspace_bytes);
 

@@ -254,7 +254,7 @@ int sgemm_f8_rmsnorm(int type, int w_type, int64_t rows, int64_t cols, const voi
     const Operand outs[5] = {oh, oy, oq, os, ors}, ins[3] = {ox, orr, ow};
     if (aliased(outs, ins, 0, 0b011u))
         return SGEMM_ERR_ALIAS;
-    if (rows * 1024 > kMaxWorkItems)
+    if (rmsnorm_work_items(rows, cols) > kMaxWorkItems)
         return SGEMM_ERR_INVALID_VALUE;
     const int dev = sgemm_f32_device_status();
     if (dev != SGEMM_OK)

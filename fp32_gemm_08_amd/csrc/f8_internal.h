@@ -81,6 +81,7 @@ struct NormArgs {
     float eps;
     int w_f32;              // W is FP32 (else of the rows' type)
 };
+int64_t rmsnorm_work_items(int64_t rows, int64_t cols);  // of its launch
 hipError_t launch_rmsnorm(const NormArgs &a, int type, hipStream_t s);
 
 struct NormBwdArgs {

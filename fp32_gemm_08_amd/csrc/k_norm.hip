@@ -265,9 +265,14 @@ struct Fwd {
     hipStream_t s;
     template <typename T, int NT, int L, int V> void run()
     {
-        constexpr int64_t ROWS = NT / L;
-        rmsnorm_kernel<T, NT, L, V><<<(unsigned)((a.rows + ROWS - 1) / ROWS), NT, 0, s>>>(a);
+        rmsnorm_kernel<T, NT, L, V><<<(unsigned)ceil_div(a.rows, NT / L), NT, 0, s>>>(a);
     }
+};
+// Work-items of that launch.
+struct Items {
+    int64_t rows;
+    int64_t *out;
+    template <typename T, int NT, int L, int V> void run() { *out = ceil_div(rows, NT / L) * NT; }
 };
 struct Bwd {
     const NormBwdArgs &a;
@@ -311,6 +316,13 @@ hipError_t launch_rmsnorm(const NormArgs &a, int type, hipStream_t s)
 {
     by_type(type, a.cols, Fwd{a, s});
     return hipGetLastError();
+}
+
+int64_t rmsnorm_work_items(int64_t rows, int64_t cols)
+{
+    int64_t n = 0;
+    by_cols<float>((int)cols, Items{rows, &n});
+    return n;
 }
 
 int64_t rmsnorm_bwd_groups(int64_t rows, int64_t cols)

@@ -98,7 +98,8 @@ int sgemm_f8_gemm_workspace(int b_block, int64_t M, int64_t N, int64_t K, int al
  *   QT  cols x rows, blocks of X^T (scales ST as above for cols x rows): the
  *       operand of a product that sums over X's rows.
  * With SGEMM_F8_TILE both hold the same values.  Rows or cols of 0: nothing is
- * touched.  Padding columns of Q and QT are not written.
+ * touched.  Padding columns of Q and QT are not written.  More than 2^24 - 1 tiles
+ * of 128 x 128 are beyond one launch: SGEMM_ERR_INVALID_VALUE.
  */
 int sgemm_f8_quantize(int block, int format, int x_type, int64_t rows, int64_t cols, const void *X, int64_t ldx,
                       void *Q, int64_t ldq, float *S, int64_t lds, void *QT, int64_t ldqt, float *ST,
@@ -113,7 +114,10 @@ int sgemm_f8_quantize(int block, int format, int x_type, int64_t rows, int64_t c
  * and rstd (rows FP32 values, for the backward pass) may each be NULL, and what
  * is NULL is not written.  H may be X or R itself (same pointer and leading
  * dimension); other overlaps of an output are SGEMM_ERR_ALIAS.
- * cols <= SGEMM_RMSNORM_MAX_COLS, eps >= 0 and finite.
+ * cols <= SGEMM_RMSNORM_MAX_COLS, eps >= 0 and finite.  Rows or cols of 0: nothing
+ * is touched.  A row is held by 16 work-items up to 128 columns, 32 up to 256, 64 up
+ * to 1024, 256 up to 4096, 512 up to 8192 and 1024 above; a call whose rows need more
+ * than one launch's 2^32 - 1 of them is SGEMM_ERR_INVALID_VALUE.
  */
 #define SGEMM_RMSNORM_MAX_COLS 32768
 int sgemm_f8_rmsnorm(int type, int w_type, int64_t rows, int64_t cols, const void *X, int64_t ldx, const void *R,

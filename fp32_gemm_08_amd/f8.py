@@ -113,9 +113,10 @@ def _tables():
     import torch
 
     _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
-    _FORMAT_OF = {torch.float8_e4m3fn: 1, torch.float8_e5m2: 2}
     _TYPE_OF = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
     _F32 = {torch.float32: 0}
+    # last: another thread's first call takes it as the sign that all are there
+    _FORMAT_OF = {torch.float8_e4m3fn: 1, torch.float8_e5m2: 2}
 
 
 def _matrix(name, t, table, device):

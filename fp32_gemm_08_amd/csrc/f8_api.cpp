@@ -143,8 +143,6 @@ int sgemm_f8_gemm(int format_a, int format_b, int b_block, int c_type, int64_t M
     if (!product && beta == 1.0f)
         return SGEMM_OK;
     if (!product) {
-        if (M * 256 > kMaxWorkItems)
-            return SGEMM_ERR_INVALID_VALUE;
         const int dev = sgemm_f32_device_status();
         if (dev != SGEMM_OK)
             return dev;

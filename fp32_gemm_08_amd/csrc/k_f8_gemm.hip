@@ -136,11 +136,11 @@ __global__ __launch_bounds__(G::NT) void f8_tile_kernel(F8GemmArgs g)
 }
 
 template <typename T>
-__global__ __launch_bounds__(256) void f8_scale_kernel(T *C, int64_t ldc, int cols, float beta)
+__global__ __launch_bounds__(256) void f8_scale_kernel(T *C, int64_t ldc, int rows, int cols, float beta)
 {
-    const int64_t row = blockIdx.x;
-    for (int64_t c = threadIdx.x; c < cols; c += 256)
-        C[row * ldc + c] = (T)(beta != 0.0f ? beta * (float)C[row * ldc + c] : 0.0f);
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x)
+        for (int64_t c = threadIdx.x; c < cols; c += 256)
+            C[row * ldc + c] = (T)(beta != 0.0f ? beta * (float)C[row * ldc + c] : 0.0f);
 }
 
 // C <- alpha * (the splits' partial sums, in order) + beta * C.
@@ -337,12 +337,13 @@ hipError_t launch_f8_gemm(F8GemmArgs a, const F8GemmPlan &p, int format_a, int f
 
 hipError_t launch_f8_scale(void *C, int64_t ldc, int rows, int cols, int c_type, float beta, hipStream_t s)
 {
+    const unsigned grid = (unsigned)std::min(rows, 1 << 20);  // (within one launch's work-items)
     if (c_type == SGEMM_TYPE_F32)
-        f8_scale_kernel<<<(unsigned)rows, 256, 0, s>>>(static_cast<float *>(C), ldc, cols, beta);
+        f8_scale_kernel<<<grid, 256, 0, s>>>(static_cast<float *>(C), ldc, rows, cols, beta);
     else if (c_type == SGEMM_TYPE_FP16)
-        f8_scale_kernel<<<(unsigned)rows, 256, 0, s>>>(static_cast<_Float16 *>(C), ldc, cols, beta);
+        f8_scale_kernel<<<grid, 256, 0, s>>>(static_cast<_Float16 *>(C), ldc, rows, cols, beta);
     else
-        f8_scale_kernel<<<(unsigned)rows, 256, 0, s>>>(static_cast<__bf16 *>(C), ldc, cols, beta);
+        f8_scale_kernel<<<grid, 256, 0, s>>>(static_cast<__bf16 *>(C), ldc, rows, cols, beta);
     return hipGetLastError();
 }
 

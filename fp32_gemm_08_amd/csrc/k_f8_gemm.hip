@@ -4,15 +4,20 @@
 //
 //   C[m][n] = alpha * sum_b sA[b][m] * sB[b][n] * (sum_{k in b} qA[m][k] * qB[n][k])
 //
-// A 16-bit C is computed by v_mfma_f32_16x16x128_f8f6f4.  That instruction
-// adds products in groups of 8, each group aligned to its largest product with
-// 13 bits kept below it (measured: 2^16 + 8 keeps the 8, 2^16 + 7 loses the 7;
-// on normally distributed operands the sum of 128 is off by 1.5e-5 of its
-// size), far below a 16-bit C's half step of 2^-9 or 2^-12, at twice the rate
-// of the 16-bit instructions.  An FP32 C is meant to hold more than that (a
-// gradient that is accumulated over many calls): its 8-bit operands are turned
-// into bf16, which holds every e4m3 and e5m2 value, and go through
-// v_mfma_f32_16x16x32_bf16, whose sums are FP32 (1e-8 on the same operands).
+// A 16-bit C is computed by v_mfma_f32_16x16x128_f8f6f4, at twice the rate of the
+// 16-bit instructions.  That instruction adds products in groups of 8, each group
+// aligned to its largest product with 13 bits kept below it (measured: 2^16 + 8
+// keeps the 8, 2^16 + 7 loses the 7).  Seven products of a group lose at most 2^-13
+// of the largest each, so a k-block's sum is off by at most 7 * 2^-13 = 8.5e-4 of
+// sum |qA qB|: below a bf16 C's half step of 2^-8, above an fp16 C's of 2^-11.  The
+// losses mostly cancel: on normally distributed operands the sum of 128 is off by
+// 1.5e-5 of its size (2-norm of the errors over that of the sums).  Relative to a sum
+// whose products cancel it is more, and there it, not C's type, decides the error.
+// An FP32 C is meant to hold more than that (a gradient that is accumulated over many
+// calls): its 8-bit operands are turned into bf16, which holds every e4m3 and e5m2
+// value, and go through v_mfma_f32_16x16x32_bf16, whose sums are FP32 (1e-8 on the
+// same operands, in the same measure; the FP32 additions over the k-blocks bring C to
+// 4e-8 at K = 128 and 1e-7 at K = 16384).
 //
 // The instructions take rows of B as their first operand and rows of A as their
 // second, so that lane l holds C[m = l % 16][n = 4*(l/16) .. +3]: four
@@ -189,9 +194,13 @@ constexpr int64_t kMaxJoin = int64_t{64} << 20;  // bytes of partial sums a call
 // The constants are measured, bf16 C: 64 x 64 tiles 1024^3 7.4 us, 256 x 4096 x 4096
 // 16.1; 128 x 64 512 x 4096 x 1024 8.9, x 4096 20.4; 128 x 128 2048^3 15.1, 1024 x
 // 4096 x 4096 25.3; 256 x 256 4096 x 4096 x 1024 22.1, 4096^3 59.6; joining 2 MB 3.5,
-// 16 MB 10.5.  Of 28 shapes from 65 x 1024 x 1024 to 8192 x 8192 x 1024, timed with
-// every tile and 1, 2, 4 and 8 parts, the estimate takes the fastest or one within 5%.
-// (An FP32 C takes about twice the step with each tile.)  `us` is the estimate.
+// 16 MB 10.5.  28 shapes from 65 x 1024 x 1024 to 8192 x 8192 x 1024 were timed with
+// every tile and 1 to 16 parts (profiles/f8_tile_choice_sweep.md).  Of a bf16 C and tile
+// scales the estimate takes the fastest or one within 2.2% but for two shapes: 128 x 512
+// x 16384 17.2 us where 14.9 is possible, 256 x 256 x 4096 10.5 where 9.8 is.  It does
+// not know an FP32 C, which takes about twice the step with each tile: there, with row
+// scales, it is within 2% but for 512 x 4096 x 16384 (91.3, possible 84.7) and 2048 x
+// 2048 x 16384 (151, 140).  `us` is the estimate.
 static F8GemmPlan plan_tiles(int64_t M, int64_t N, int64_t K, int64_t room, double &us)
 {
     static const struct { int kid, bm, bn; double step, ends; } kTiles[4] = {{KID_F8_S, 64, 64, 0.36, 2.4},
@@ -231,7 +240,11 @@ F8GemmPlan f8_gemm_plan(bool row_b, int64_t M, int64_t N, int64_t K, bool aligne
     aligned = aligned && K <= F8_MAX_LD;  // (rows that do not overlap lie at least K apart)
     // few rows of A; of operands at other alignments up to 16 (N = K = 4096, through the
     // wavefronts' registers / through the 64 x 64 tile: 1 row 11.3 / 17.3 us, 16 rows
-    // 17.6 / 17.7, 32 rows 25.0 / 18.0)
+    // 17.6 / 17.7, 32 rows 25.0 / 18.0).  Aligned up to 64 (through registers / the fastest
+    // tile, bf16 C and tile scales; FP32 C and row scales): 64 x 4096 x 4096 12.9 / 13.0;
+    // 14.2 / 14.9, 64 x 1024 x 1024 5.6 / 6.8; 5.7 / 8.8, 32 x 4096 x 4096 9.2 / 11.7; 9.3 /
+    // 13.7.  The rule does not look at N and K, and loses with many columns or a deep k:
+    // 64 x 16384 x 4096 24.4 / 16.3; 48.6 / 23.9, 64 x 1024 x 16384 39.8 / 14.8; 42.2 / 18.0
     if (M <= (aligned ? 64 : 16)) {
         p.kid = KID_F8_SKINNY;
         p.tiles_m = 1;

@@ -155,6 +155,8 @@ __global__ __launch_bounds__(512) void f8_skinny_kernel(F8GemmArgs g)
 template <int FM, int FN, bool ROWB>
 void launch(const F8GemmArgs &a, int fa, int fb, hipStream_t s)
 {
+    // k-blocks in flight; of the largest operands (4 and 4 blocks of 16 rows) one is already
+    // more than the 256 registers hold: 15 are spilled with a 16-bit C, 39 with an FP32 C
     constexpr int DEPTH = FM + FN <= 2 ? 4 : FM + FN <= 5 ? 2 : 1;
     const dim3 grid((unsigned)a.tiles_n), block(512);
     on_format(fa, [&](auto FA) { on_format(fb, [&](auto FB) { on_bool(a.c_type == SGEMM_TYPE_F32, [&](auto EX) {

@@ -279,7 +279,11 @@ struct Bwd {
     hipStream_t s;
     template <typename T, int NT, int L, int V> void run()
     {
-        // with 1024 work-items of 128 registers, the 32-bit rows leave no room for the next one
+        // 1024 work-items have 128 registers each, which is too few above 8192 columns.  With
+        // two pieces the next row is held in 16 bits only (190 registers are spilled of bf16
+        // rows, 169 of fp16; of 32-bit rows 6, without it); with four 660 and more are spilled
+        // either way.  Measured: 8192 x 8192 bf16, nothing spilled, 101 us (5.3 TB/s); 4096 x
+        // 16384 bf16 123 (4.4); 2048 x 32768 bf16 293 (1.8), fp32 430 (2.5).
         constexpr bool AHEAD = NT < 1024 || (V == 2 && sizeof(T) == 2);
         rmsnorm_bwd_kernel<T, NT, L, V, AHEAD><<<(unsigned)a.groups, NT, 0, s>>>(a);
     }

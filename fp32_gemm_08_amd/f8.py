@@ -7,6 +7,12 @@ NULL) and ``stream`` is a hipStream_t as an integer.  ``f8_gemm``,
 torch tensors: outputs are the caller's tensors, written in place, leading
 dimensions are row strides, and the stream is torch's current one.  torch is
 used for device memory and streams only; there is no fallback.
+
+The tensor functions are no part of torch's gradient tracking: inputs that require
+gradients are taken as they are, outputs carry no history, and writing them does not
+move their version counters, so torch does not notice when a tensor that it saved for
+a backward pass is overwritten.  A program that trains calls the backward functions
+itself (or wraps both directions in a torch.autograd.Function) and keeps what they read.
 """
 from __future__ import annotations
 

@@ -49,8 +49,12 @@ typedef enum { SGEMM_TYPE_F32 = 0, SGEMM_TYPE_FP16 = 1, SGEMM_TYPE_BF16 = 2 } sg
  * rounded once.  With an FP32 C the k-block's sum is FP32 too (the operands go
  * through the 16-bit matrix cores, which hold every 8-bit value exactly); with
  * a 16-bit C it is that of the 8-bit matrix cores, which add products in groups
- * of 8 consecutive k, a product keeping 13 bits below the largest of its group.
- * beta == 0: C is not read.  alpha == 0 or
+ * of 8 consecutive k, a product keeping 13 bits below the largest of its group:
+ * off by at most 7 * 2^-13 of the sum of the products' absolute values, and by
+ * 1.5e-5 of its size on normally distributed operands.  Where products cancel to
+ * less than that, ask for an FP32 C.  The product sA * sB loses bits below 2^-126
+ * (two e5m2 blocks whose maxima multiply to less than 2^-94, two e4m3 blocks to
+ * less than 2^-108) and is infinite from 2^128 on.  alpha == 0 or
  * K == 0: C <- beta * C and A, B and their scales are not read.
  *
  * A, lda, B and ldb may have any alignment.  Bases and leading dimensions that

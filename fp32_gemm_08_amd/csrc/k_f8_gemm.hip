@@ -195,11 +195,12 @@ constexpr int64_t kMaxJoin = int64_t{64} << 20;  // bytes of partial sums a call
 // 16.1; 128 x 64 512 x 4096 x 1024 8.9, x 4096 20.4; 128 x 128 2048^3 15.1, 1024 x
 // 4096 x 4096 25.3; 256 x 256 4096 x 4096 x 1024 22.1, 4096^3 59.6; joining 2 MB 3.5,
 // 16 MB 10.5.  28 shapes from 65 x 1024 x 1024 to 8192 x 8192 x 1024 were timed with
-// every tile and 1 to 16 parts.  Of a bf16 C and tile scales the estimate takes the fastest or one within 2.2% but for two shapes: 128 x 512
-// x 16384 17.2 us where 14.9 is possible, 256 x 256 x 4096 10.5 where 9.8 is.  It does
-// not know an FP32 C, which takes about twice the step with each tile: there, with row
-// scales, it is within 2% but for 512 x 4096 x 16384 (91.3, possible 84.7) and 2048 x
-// 2048 x 16384 (151, 140).  `us` is the estimate.
+// every tile and 1 to 16 parts.  Of a bf16 C and tile scales the estimate takes the
+// fastest or one within 2.2% but for two: 128 x 512 x 16384 17.2 us where 14.9 is
+// possible, 256 x 256 x 4096 10.5 where 9.8 is.  It does not know an FP32 C, which takes
+// about twice the step with each tile: there, with row scales, it is within 2% but for
+// 512 x 4096 x 16384 (91.3, possible 84.7) and 2048 x 2048 x 16384 (151, 140).  `us` is
+// the estimate.
 static F8GemmPlan plan_tiles(int64_t M, int64_t N, int64_t K, int64_t room, double &us)
 {
     static const struct { int kid, bm, bn; double step, ends; } kTiles[4] = {{KID_F8_S, 64, 64, 0.36, 2.4},

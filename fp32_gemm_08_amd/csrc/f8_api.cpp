@@ -1,85 +1,11 @@
 // C ABI of the 8-bit block-scaled family (include/sgemm_f8.h): argument checks
 // and launches.  Nothing here allocates, copies or synchronises.
-#include "f8_internal.h"
+#include "api_checks.h"
 #include "sgemm_f8.h"
-
-#include <cmath>
-#include <limits>
 
 using namespace sgemm;
 
 namespace {
-
-constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1025;
-constexpr int64_t kAnyRoom = std::numeric_limits<int64_t>::max();
-constexpr int64_t kMaxWorkItems = (int64_t{1} << 32) - 1;
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-int type_bytes(int t) { return t == SGEMM_TYPE_F32 ? 4 : 2; }
-bool known_type(int t) { return t == SGEMM_TYPE_F32 || t == SGEMM_TYPE_FP16 || t == SGEMM_TYPE_BF16; }
-bool known_format(int f) { return f == SGEMM_F8_E4M3 || f == SGEMM_F8_E5M2; }
-bool known_block(int b) { return b == SGEMM_F8_ROW || b == SGEMM_F8_TILE; }
-bool dim_ok(int64_t d) { return d >= 0 && d <= kMaxDim; }
-bool on(const void *p, int bytes) { return p != nullptr && reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }
-
-// A rows x cols operand of `size`-byte elements: what its bytes span, and
-// whether every row starts on a `to`-byte boundary.
-struct Operand {
-    const void *p;
-    int64_t rows, cols, ld;
-    int size;
-    // A leading dimension that holds a row, and a span within int64.
-    bool shape_ok() const
-    {
-        return ld >= (cols > 1 ? cols : 1) && (rows <= 1 || ld <= std::numeric_limits<int64_t>::max() / 8 / rows);
-    }
-    int64_t bytes() const { return rows == 0 || cols == 0 ? 0 : ((rows - 1) * ld + cols) * size; }
-    bool present() const { return on(p, size); }
-    bool rows_on(int to) const
-    {
-        return reinterpret_cast<uintptr_t>(p) % (uintptr_t)to == 0 && (rows <= 1 || ld * size % to == 0);
-    }
-    // The same elements at the same places (an update in place).
-    bool same(const Operand &o) const
-    {
-        return p == o.p && size == o.size && (rows <= 1 || ld == o.ld);
-    }
-};
-
-bool overlap(const Operand &a, const Operand &b)
-{
-    if (a.p == nullptr || b.p == nullptr || a.bytes() == 0 || b.bytes() == 0)
-        return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return x < y + (uintptr_t)b.bytes() && y < x + (uintptr_t)a.bytes();
-}
-
-// Whether some output overlaps another operand: every output against every
-// input (in place where `in_place` allows that pair) and every other output.
-template <int NO, int NI>
-bool aliased(const Operand (&out)[NO], const Operand (&in)[NI], int in_place_out, unsigned in_place_in)
-{
-    for (int i = 0; i < NO; ++i) {
-        for (int j = i + 1; j < NO; ++j)
-            if (overlap(out[i], out[j]))
-                return true;
-        for (int j = 0; j < NI; ++j)
-            if (overlap(out[i], in[j]) && !(i == in_place_out && (in_place_in >> j & 1) && out[i].same(in[j])))
-                return true;
-    }
-    return false;
-}
-
-// A scale array of a rows x cols operand.
-Operand scales(const float *p, int block, int64_t rows, int64_t cols, int64_t ld)
-{
-    if (block == SGEMM_F8_ROW)
-        return Operand{p, ceil_div(cols, F8_BLOCK), rows, ld, 4};
-    return Operand{p, ceil_div(rows, F8_BLOCK), ceil_div(cols, F8_BLOCK), ld, 4};
-}
-
-int finish(hipError_t e) { return e == hipSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH; }
 
 int threads_of(int kid) { return kid == KID_F8_ANY ? 256 : 512; }
 
@@ -226,6 +152,46 @@ int sgemm_f8_quantize(int block, int format, int x_type, int64_t rows, int64_t c
     a.tiles_c = 0;
     (void)hipGetLastError();
     return finish(launch_f8_quantize(a, block == SGEMM_F8_TILE, format, x_type, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int sgemm_f8_requantize(int format_x, int format, int64_t rows, int64_t cols, const void *X, int64_t ldx,
+                        const float *SX, int64_t ldsx, void *QT, int64_t ldqt, float *ST, int64_t ldst, void *stream)
+{
+    if (!known_format(format_x) || !known_format(format) || !dim_ok(rows) || !dim_ok(cols))
+        return SGEMM_ERR_INVALID_VALUE;
+    const Operand ox{X, rows, cols, ldx, 1}, oqt{QT, cols, rows, ldqt, 1};
+    const Operand osx = scales(SX, SGEMM_F8_ROW, rows, cols, ldsx), ost = scales(ST, SGEMM_F8_ROW, cols, rows, ldst);
+    if (!ox.shape_ok() || !osx.shape_ok() || !oqt.shape_ok() || !ost.shape_ok())
+        return SGEMM_ERR_INVALID_VALUE;
+    if (rows == 0 || cols == 0)
+        return SGEMM_OK;
+    if (!ox.present() || !osx.present() || !oqt.present() || !ost.present())
+        return SGEMM_ERR_INVALID_VALUE;
+    const Operand outs[2] = {oqt, ost}, ins[2] = {ox, osx};
+    if (aliased(outs, ins, -1, 0))
+        return SGEMM_ERR_ALIAS;
+    if (ceil_div(rows, F8_BLOCK) * ceil_div(cols, F8_BLOCK) * 256 > kMaxWorkItems)
+        return SGEMM_ERR_INVALID_VALUE;
+    const int dev = sgemm_f32_device_status();
+    if (dev != SGEMM_OK)
+        return dev;
+    F8QuantArgs a;
+    a.X = X;
+    a.Q = nullptr;
+    a.QT = static_cast<uint8_t *>(QT);
+    a.S = nullptr;
+    a.ST = ST;
+    a.ldx = ldx;
+    a.ldq = a.lds = 0;
+    a.ldqt = ldqt;
+    a.ldst = ldst;
+    a.rows = (int)rows;
+    a.cols = (int)cols;
+    a.tiles_c = 0;
+    a.SX = SX;
+    a.ldsx = ldsx;
+    (void)hipGetLastError();
+    return finish(launch_f8_requantize(a, format_x, format, reinterpret_cast<hipStream_t>(stream)));
 }
 
 int sgemm_f8_rmsnorm(int type, int w_type, int64_t rows, int64_t cols, const void *X, int64_t ldx, const void *R,

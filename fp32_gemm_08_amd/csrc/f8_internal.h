@@ -68,7 +68,11 @@ struct F8QuantArgs {
     int64_t ldx, ldq, lds, ldqt, ldst;
     int rows, cols;
     int tiles_c;            // tiles along the columns
+    const float *SX = nullptr;  // scales of X's row blocks, where it is in 8 bits itself
+    int64_t ldsx = 0;
 };
+// The transposed output alone, from an X in 8 bits with row blocks.
+hipError_t launch_f8_requantize(F8QuantArgs a, int format_x, int format, hipStream_t s);
 hipError_t launch_f8_quantize(F8QuantArgs a, bool tile, int format, int x_type, hipStream_t s);
 
 struct NormArgs {

@@ -234,6 +234,51 @@ __device__ __forceinline__ void row_store8b(uint8_t *row, int c, int cols, uint3
         *p = (uint8_t)lo;
 }
 
+// Bytes c .. c+7 of a row of `cols`, zero past its end; a shorter last piece as in row_raw8.
+template <bool STREAM>
+__device__ __forceinline__ f8_u32x2 row_raw8b(const uint8_t *row, int c, int cols)
+{
+    typedef f8_u32x2 u32x2_any __attribute__((aligned(1)));
+    if (c + 8 <= cols) {
+        const u32x2_any *p = reinterpret_cast<const u32x2_any *>(row + c);
+        if constexpr (STREAM)
+            return __builtin_nontemporal_load(p);
+        else
+            return *p;
+    }
+    uint64_t v = 0;
+    if (c < cols) {
+        if (cols >= 8) {
+            const f8_u32x2 d = *reinterpret_cast<const u32x2_any *>(row + cols - 8);
+            v = (d[0] | (uint64_t)d[1] << 32) >> (8 * (c + 8 - cols));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 7; ++i)
+                if (c + i < cols)
+                    v |= (uint64_t)row[c + i] << (8 * i);
+        }
+    }
+    return f8_u32x2{(uint32_t)v, (uint32_t)(v >> 32)};
+}
+// What 8 bytes of that format stand for, without their scale.
+template <int FMT>
+__device__ __forceinline__ void f8_unpack8(f8_u32x2 q, float (&v)[8])
+{
+    typedef float f2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        f2 lo, hi;
+        if constexpr (FMT == 0) {
+            lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[i], false);
+            hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[i], true);
+        } else {
+            lo = __builtin_amdgcn_cvt_pk_f32_bf8((int)q[i], false);
+            hi = __builtin_amdgcn_cvt_pk_f32_bf8((int)q[i], true);
+        }
+        v[4 * i] = lo[0], v[4 * i + 1] = lo[1], v[4 * i + 2] = hi[0], v[4 * i + 3] = hi[1];
+    }
+}
+
 // |x| as an unsigned number: ordered as |x| is, infinity above every finite
 // value and NaN above infinity, so that an integer maximum carries a NaN
 // through (the FP32 maximum instruction drops it).
@@ -284,6 +329,22 @@ __device__ __forceinline__ void block_scale(uint32_t bits, float &inv, float &sc
     const float a = __uint_as_float(max(bits, __float_as_uint(F8_FLOOR)));
     inv = f8_largest<FMT>() / a;
     scale = a / f8_largest<FMT>();
+}
+
+// The same for 8-bit integers with one scale.
+__device__ __forceinline__ void i8_scale(uint32_t bits, float &inv, float &scale)
+{
+    const float a = __uint_as_float(max(bits, __float_as_uint(F8_FLOOR)));
+    inv = 127.0f / a;
+    scale = a / 127.0f;
+}
+
+// To the nearest integer, ties to even; NaN (of a row that holds one, or an infinity): 0.
+__device__ __forceinline__ int i8_round(float t) { return (int)rintf(t == t ? t : 0.0f); }
+
+__device__ __forceinline__ uint32_t i8_pack4(int a, int b, int c, int d)
+{
+    return ((uint32_t)a & 0xff) | ((uint32_t)b & 0xff) << 8 | ((uint32_t)c & 0xff) << 16 | (uint32_t)d << 24;
 }
 
 }  // namespace sgemm

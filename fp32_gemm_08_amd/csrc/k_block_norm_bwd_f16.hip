@@ -1,0 +1,11 @@
+// Backward pass of the norms around a block for rows of _Float16.
+#include "block_norm_bwd.h"
+
+namespace sgemm {
+
+template <> void launch_block_norm_bwd_rows<_Float16>(const BlockNormBwdArgs &a, bool kept, bool several, hipStream_t s)
+{
+    by_cols<_Float16>(a.cols, Bwd{a, kept, several, s});
+}
+
+}  // namespace sgemm

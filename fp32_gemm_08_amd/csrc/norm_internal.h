@@ -1,0 +1,50 @@
+// Internal declarations of the norms around a block.
+#pragma once
+
+#include "f8_internal.h"
+#include "sgemm_norm.h"
+
+namespace sgemm {
+
+struct BlockNormArgs {
+    const void *X, *O, *W, *WP, *G;
+    void *H, *Y;
+    uint8_t *Q, *H8, *O8;
+    float *S, *SH, *SO, *rstd, *rstd_post;
+    int64_t ldx, ldo, ldg, ldh, ldy, ldq, lds, ldh8, ldsh, ldo8, ldso;
+    int rows, cols, gate_rows;
+    float alpha, eps;
+    int w_f32;              // W, WP and G are FP32 (else of the rows' type)
+    int q_i8;               // Q holds integers with a scale per row
+};
+hipError_t launch_block_norm(const BlockNormArgs &a, int type, hipStream_t s);
+
+struct BlockNormBwdArgs {
+    const void *DY, *DH, *H, *O, *W, *WP, *G;
+    const float *SH, *SO, *rstd, *rstd_post;
+    void *DX, *DO;
+    float *DW, *DWP, *DG;
+    float *ws;              // partial sums, see BlockNormSums
+    int64_t lddy, lddh, ldh, ldsh, ldo, ldso, ldg, lddx, lddo, lddg;
+    int rows, cols, gate_rows;
+    float alpha;
+    int w_f32;
+    int groups;             // workgroups
+    int chunk;              // consecutive rows of a walker
+};
+
+// Who sums what of the backward pass.  A walker is the work-items that hold a row (a
+// workgroup, or 16 to 64 lanes of one); it takes `chunk` consecutive rows.  With one
+// gate row for all rows a workgroup leaves the sums of dy n and of d m of all its rows.
+// With several it leaves those of dy n and of gate d m, and its walkers leave their sums
+// of d m for those gate rows of which they do not have all rows: for the first that they
+// meet at 2 * walker, for another one (the last) at 2 * walker + 1.
+struct BlockNormSums {
+    int64_t groups = 0, walkers = 0, chunk = 1;
+    bool several = false;
+    int64_t parts = 0;      // arrays of cols floats in the workspace
+};
+BlockNormSums block_norm_sums(int64_t rows, int64_t cols, int64_t gate_rows);
+hipError_t launch_block_norm_bwd(BlockNormBwdArgs a, int type, bool kept, hipStream_t s);
+
+}  // namespace sgemm

@@ -3,8 +3,8 @@
 The ``sgemm_f8_*`` functions keep the C names and arguments of
 ``include/sgemm_f8.h``; pointers are plain integers (device addresses, 0 for
 NULL) and ``stream`` is a hipStream_t as an integer.  ``f8_gemm``,
-``f8_quantize``, ``rmsnorm`` and ``rmsnorm_backward`` are the same calls over
-torch tensors: outputs are the caller's tensors, written in place, leading
+``f8_quantize``, ``f8_requantize``, ``rmsnorm`` and ``rmsnorm_backward`` are the
+same calls over torch tensors: outputs are the caller's tensors, written in place, leading
 dimensions are row strides, and the stream is torch's current one.  torch is
 used for device memory and streams only; there is no fallback.
 
@@ -27,7 +27,7 @@ RMSNORM_MAX_COLS = 32768
 
 # Symbols declared in include/sgemm_f8.h.
 F8_EXPORTS = ("sgemm_f8_gemm", "sgemm_f8_gemm_plan", "sgemm_f8_gemm_workspace", "sgemm_f8_quantize",
-              "sgemm_f8_rmsnorm", "sgemm_f8_rmsnorm_bwd", "sgemm_f8_rmsnorm_bwd_plan")
+              "sgemm_f8_requantize", "sgemm_f8_rmsnorm", "sgemm_f8_rmsnorm_bwd", "sgemm_f8_rmsnorm_bwd_plan")
 
 _f8 = None
 
@@ -44,6 +44,7 @@ def _load_f8():
                 ("sgemm_f8_gemm_plan", [ci, i64, i64, i64, ci, pi, pl, pl, pl, pl]),
                 ("sgemm_f8_gemm_workspace", [ci, i64, i64, i64, ci, pl]),
                 ("sgemm_f8_quantize", [ci, ci, ci, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp]),
+                ("sgemm_f8_requantize", [ci, ci, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp]),
                 ("sgemm_f8_rmsnorm", [ci, ci, i64, i64, vp, i64, vp, i64, vp, f32, vp, i64, vp, i64, vp, i64, vp, i64,
                                       vp, vp]),
                 ("sgemm_f8_rmsnorm_bwd", [ci, ci, i64, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, vp, vp, i64,
@@ -83,6 +84,11 @@ def sgemm_f8_quantize(block, format, x_type, rows, cols, X, ldx, Q, ldq, S, lds,
     """X -> its 8-bit values and scales, and (QT) those of X^T.  Returns the status code."""
     return _load_f8().sgemm_f8_quantize(block, format, x_type, rows, cols, X, ldx, Q, ldq, S, lds, QT, ldqt, ST, ldst,
                                         stream)
+
+
+def sgemm_f8_requantize(format_x, format, rows, cols, X, ldx, SX, ldsx, QT, ldqt, ST, ldst, stream=0) -> int:
+    """8-bit X with row blocks -> 8-bit X^T with row blocks.  Returns the status code."""
+    return _load_f8().sgemm_f8_requantize(format_x, format, rows, cols, X, ldx, SX, ldsx, QT, ldqt, ST, ldst, stream)
 
 
 def sgemm_f8_rmsnorm(type, w_type, rows, cols, X, ldx, R, ldr, W, eps, H, ldh, Y, ldy, Q, ldq, S, lds, rstd,
@@ -264,6 +270,24 @@ def f8_quantize(X, Q=None, S=None, QT=None, ST=None, block="row", stream=None):
         raise TypeError("Q and QT must have the same format")
     _run(dev, stream, _load_f8().sgemm_f8_quantize,
          (b, fmt, xt, rows, cols, px, ldx, pq, ldq, ps, lds, pqt, ldqt, pst, ldst))
+
+
+def f8_requantize(X, SX, QT, ST, stream=None):
+    """What X (rows, cols; float8_e4m3fn or float8_e5m2) and its scales SX
+    (ceil(cols/128), rows) stand for -> QT (cols, rows; either format) and ST
+    (ceil(rows/128), cols), its transpose with one scale per 128 values along the
+    rows of X: a product over the rows takes it, without the 16-bit values having
+    been kept.
+    """
+    dev = _device(X)
+    fx, rows, cols, px, ldx = _matrix("X", X, _FORMAT_OF, dev)
+    fq, r, c, pq, ldq = _matrix("QT", QT, _FORMAT_OF, dev)
+    if (r, c) != (cols, rows):
+        raise ValueError(f"QT has shape {(r, c)}, not {(cols, rows)}")
+    psx, ldsx = _scale("SX", SX, (_blocks(cols), rows), dev)
+    pst, ldst = _scale("ST", ST, (_blocks(rows), cols), dev)
+    _run(dev, stream, _load_f8().sgemm_f8_requantize,
+         (fx, fq, rows, cols, px, ldx, psx, ldsx, pq, ldq, pst, ldst))
 
 
 def rmsnorm(X, W, eps=1e-6, residual=None, H=None, Y=None, Q=None, S=None, rstd=None, stream=None):

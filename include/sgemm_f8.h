@@ -110,6 +110,20 @@ int sgemm_f8_quantize(int block, int format, int x_type, int64_t rows, int64_t c
                       int64_t ldst, void *stream);
 
 /*
+ * Values that are kept in 8 bits with blocks along their rows, laid out for a product
+ * that sums over the rows (the weight's gradient, from the activations that the
+ * forward product read):  X rows x cols in format_x, row blocks, scales SX (as above
+ * for rows x cols)  ->  QT cols x rows in `format`, row blocks of X^T, scales ST (as
+ * above for cols x rows).  Each value is taken as fl(q * s) in FP32 and quantised as
+ * sgemm_f8_quantize does; a block that holds a value of X's NaN or infinite blocks gets
+ * a NaN or infinite scale.  Rows or cols of 0: nothing is touched.  Padding columns of
+ * QT are not written.  At most 2^24 - 1 tiles of 128 x 128.  Outputs overlap no
+ * operand and not each other: SGEMM_ERR_ALIAS.
+ */
+int sgemm_f8_requantize(int format_x, int format, int64_t rows, int64_t cols, const void *X, int64_t ldx,
+                        const float *SX, int64_t ldsx, void *QT, int64_t ldqt, float *ST, int64_t ldst, void *stream);
+
+/*
  * Root-mean-square norm of each row, after an addition, with an 8-bit output:
  *     h = x + r      rstd = 1 / sqrt(mean(h^2) + eps)      y = h * rstd * w
  * in FP32 (h enters the norm unrounded).  X, R, H and Y are rows x cols of

@@ -58,6 +58,10 @@ hipError_t launch_f8_large(const F8GemmArgs &a, int splits, int format_a, int fo
 // Few rows of A: columns per workgroup, and the launch.
 int f8_skinny_cols(bool row_b, int64_t N);
 hipError_t launch_f8_skinny(const F8GemmArgs &a, int format_a, int format_b, bool row_b, hipStream_t s);
+// The rows of A, then those of B, laid out anew with whole lines a row, zeros past K.
+constexpr int64_t F8_MAX_PACKED = int64_t{1} << 40;  // bytes of an operand that this is done for
+inline int64_t f8_packed_ld(int64_t K) { return ceil_div(K, 128) * 128; }
+hipError_t launch_f8_pack(const F8GemmArgs &a, uint8_t *to, hipStream_t s);
 // C <- beta * C for a rows x cols C of any type.
 hipError_t launch_f8_scale(void *C, int64_t ldc, int rows, int cols, int c_type, float beta, hipStream_t s);
 

@@ -6,14 +6,31 @@
 
 namespace sgemm {
 
-// 16 x 16 products of 64 values of k.  The instruction takes rows of B as its first
-// operand and rows of A as its second, so that lane l holds C[m = l % 16][n = 4*(l/16)
-// .. +3]; lane l supplies 16 consecutive values of row l % 16 of each, which 16 is free
-// as long as both agree.
-__device__ __forceinline__ f8_i32x4 i8_mma(f8_i32x4 b, f8_i32x4 a, f8_i32x4 c)
-{
-    return __builtin_amdgcn_mfma_i32_16x16x64_i8(b, a, c, 0, 0, 0);
-}
+// Blocks of MB x MB elements of C.  The instructions take rows of B as their first operand
+// and rows of A as their second: lane l holds row m = l % MB of C, and of its columns groups
+// of 4 consecutive ones, the first at 4 * (l / MB), each next one 256 / MB further.  Lane l
+// supplies of row l % MB of each operand 16 consecutive values for a slice of 1024 / MB
+// values of k, at chunk l / MB of the slice (which place is free as long as both agree).
+typedef int i8_i32x16 __attribute__((ext_vector_type(16)));
+template <int MB> struct I8Block;
+template <> struct I8Block<16> {
+    typedef f8_i32x4 Acc;
+    static __device__ __forceinline__ Acc mma(f8_i32x4 b, f8_i32x4 a, Acc c)
+    {
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(b, a, c, 0, 0, 0);
+    }
+};
+template <> struct I8Block<32> {
+    typedef i8_i32x16 Acc;
+    static __device__ __forceinline__ Acc mma(f8_i32x4 b, f8_i32x4 a, Acc c)
+    {
+        return __builtin_amdgcn_mfma_i32_32x32x32_i8(b, a, c, 0, 0, 0);
+    }
+};
+template <int MB> struct I8Frag {
+    static constexpr int NS = MB / 8;           // slices of a k-block of 128
+    f8_i32x4 v[NS];
+};
 
 // Columns n .. n+7 of row m of C <- alpha * (v * SA[m]) * SB[n] + beta * C.
 template <typename T>
@@ -55,20 +72,23 @@ __device__ __forceinline__ void i8_put_part(int *row, int n, int cols, const int
     row_store8(reinterpret_cast<float *>(row), n, cols, o);
 }
 
-// A wavefront's 16 rows of WN columns of C, of which lane l holds row l % 16, columns
-// 16j + 4*(l/16) .. +3: through `buf` (16 x (WN + 4) words of this wavefront's own), so
-// that WN/8 lanes write one row together.  `part`: this split's partial sums.
-template <int FN>
-__device__ __forceinline__ void i8_store_rows(const I8GemmArgs &g, int *buf, int m, int n, const f8_i32x4 (&acc)[FN],
-                                              int *part = nullptr)
+// A wavefront's MB rows of FN blocks of C through `buf` (MB x (MB FN + 4) words of this
+// wavefront's own), so that the lanes of a row write it together.  `part`: this split's
+// partial sums.
+template <int MB, int FN>
+__device__ __forceinline__ void i8_store_rows(const I8GemmArgs &g, int *buf, int m, int n,
+                                              const typename I8Block<MB>::Acc (&acc)[FN], int *part = nullptr)
 {
-    constexpr int PITCH = 16 * FN + 4, LANES = 2 * FN;  // lanes of a row
+    constexpr int PITCH = MB * FN + 4, LANES = MB * FN / 8;  // lanes of a row
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int j = 0; j < FN; ++j)
-        *reinterpret_cast<f8_i32x4 *>(buf + (lane & 15) * PITCH + 16 * j + 4 * (lane >> 4)) = acc[j];
+#pragma unroll
+        for (int x = 0; x < MB * MB / 256; ++x)
+            *reinterpret_cast<f8_i32x4 *>(buf + lane % MB * PITCH + MB * j + 4 * (lane / MB) + 256 / MB * x) =
+                f8_i32x4{acc[j][4 * x], acc[j][4 * x + 1], acc[j][4 * x + 2], acc[j][4 * x + 3]};
 #pragma unroll 1
-    for (int e = lane; e < 16 * LANES; e += 64) {
+    for (int e = lane; e < MB * LANES; e += 64) {
         const int r = e / LANES, c = 8 * (e % LANES);
         if (m + r >= g.M || n + c >= g.N)
             continue;

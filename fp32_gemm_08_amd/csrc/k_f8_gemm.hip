@@ -180,10 +180,8 @@ __global__ __launch_bounds__(256) void f8_pack_kernel(F8GemmArgs g, uint8_t *to,
             valid == 16 ? *reinterpret_cast<const f8_i32x4_any *>(p) : load16_any(p, valid);
     }
 }
-int64_t f8_packed_ld(int64_t K) { return ceil_div(K, 128) * 128; }
 
 typedef F8Geo<64, 64, 2, 2> GS;
-constexpr int64_t kMaxPacked = int64_t{1} << 40;  // bytes of a packed operand
 constexpr int64_t kMaxJoin = int64_t{64} << 20;  // bytes of partial sums a call may ask for
 
 }  // namespace
@@ -256,7 +254,7 @@ F8GemmPlan f8_gemm_plan(bool row_b, int64_t M, int64_t N, int64_t K, bool aligne
     p.kid = KID_F8_ANY;
     p.tiles_m = ceil_div(M, GS::BM);
     p.tiles_n = ceil_div(N, GS::BN);
-    if (may_pack && N > 1 && f8_packed_ld(K) <= F8_MAX_LD && M <= kMaxPacked / f8_packed_ld(K) && N <= kMaxPacked / f8_packed_ld(K)) {
+    if (may_pack && N > 1 && f8_packed_ld(K) <= F8_MAX_LD && M <= F8_MAX_PACKED / f8_packed_ld(K) && N <= F8_MAX_PACKED / f8_packed_ld(K)) {
         const int64_t pack = (M + N) * f8_packed_ld(K);
         if (pack <= room) {
             const F8GemmPlan q = plan_tiles(M, N, K, room - pack, us);
@@ -286,6 +284,13 @@ F8GemmPlan f8_call_plan(const F8GemmArgs &a, bool rows_on_16, bool row_b, int64_
     return f8_gemm_plan(row_b, a.M, a.N, a.K, aligned, room, near);
 }
 
+hipError_t launch_f8_pack(const F8GemmArgs &a, uint8_t *to, hipStream_t s)
+{
+    const int64_t ld = f8_packed_ld(a.K), chunks = ((int64_t)a.M + a.N) * (ld / 16);
+    f8_pack_kernel<<<(unsigned)std::min<int64_t>(ceil_div(chunks, 256), 16384), 256, 0, s>>>(a, to, ld);
+    return hipGetLastError();
+}
+
 hipError_t launch_f8_gemm(F8GemmArgs a, const F8GemmPlan &p, int format_a, int format_b, bool row_b, hipStream_t s)
 {
     a.tiles_m = (int)p.tiles_m;
@@ -296,10 +301,9 @@ hipError_t launch_f8_gemm(F8GemmArgs a, const F8GemmPlan &p, int format_a, int f
             return hipErrorInvalidValue;
     }
     if (p.pack) {
-        const int64_t ld = f8_packed_ld(a.K), chunks = ((int64_t)a.M + a.N) * (ld / 16);
+        const int64_t ld = f8_packed_ld(a.K);
         uint8_t *to = reinterpret_cast<uint8_t *>(a.ws);
-        f8_pack_kernel<<<(unsigned)std::min<int64_t>(ceil_div(chunks, 256), 16384), 256, 0, s>>>(a, to, ld);
-        const hipError_t e = hipGetLastError();
+        const hipError_t e = launch_f8_pack(a, to, s);
         if (e != hipSuccess)
             return e;
         a.A = to;

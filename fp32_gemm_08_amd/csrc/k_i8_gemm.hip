@@ -78,7 +78,7 @@ __global__ __launch_bounds__(G::NT) void i8_tile_kernel(I8GemmArgs g)
                 const f8_i32x4 a = read(wm * G::WM + 16 * i + l16, q + 4 * half);
 #pragma unroll
                 for (int j = 0; j < G::FN; ++j)
-                    acc[i][j] = i8_mma(b[j], a, acc[i][j]);
+                    acc[i][j] = I8Block<16>::mma(b[j], a, acc[i][j]);
             }
         }
         __syncthreads();
@@ -86,20 +86,121 @@ __global__ __launch_bounds__(G::NT) void i8_tile_kernel(I8GemmArgs g)
     int *buf = reinterpret_cast<int *>(smem) + w * G::OUT;
 #pragma unroll
     for (int i = 0; i < G::FM; ++i)
-        i8_store_rows<G::FN>(g, buf, m0 + wm * G::WM + 16 * i, n0 + wn * G::WN, acc[i]);
+        i8_store_rows<16, G::FN>(g, buf, m0 + wm * G::WM + 16 * i, n0 + wn * G::WN, acc[i]);
+}
+
+// C from the splits' partial sums, which are integers: their order does not matter.
+__global__ __launch_bounds__(256) void i8_join_kernel(I8GemmArgs g, int splits)
+{
+    const int64_t per_row = ((int64_t)g.N + 7) / 8, total = per_row * g.M;
+    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
+        const int m = (int)(e / per_row), n = 8 * (int)(e % per_row);
+        int v[8] = {};
+        for (int x = 0; x < splits; ++x) {
+            float u[8];  // (the bits of integers)
+            row_load8<false>(reinterpret_cast<const float *>(g.ws) + ((int64_t)x * g.M + m) * g.N, n, g.N, u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] += __float_as_int(u[i]);
+        }
+        i8_put8(g, m, n, v);
+    }
 }
 
 typedef F8Geo<64, 64, 2, 2> GS;
+constexpr int64_t kMaxJoin = int64_t{64} << 20;  // bytes of partial sums a call may ask for
+
+// What joining the splits' sums takes, in us.
+double join_us(int64_t bytes) { return 2.5 + (double)bytes * 0.5e-6; }
+
+// Which tile, and into how many parts the k-blocks are split: the least estimate of
+//     2 us + the larger of (the rounds of workgroups that the 256 CUs take) and (2.2 us and
+//     the operands' and C's bytes at 5 TB/s) + what joining the parts takes.
+// A round of one workgroup on each CU takes (k-blocks of a part * step + ends); the 64 x 64
+// tile leaves room for two, and a round of two takes (k-blocks * step2 + ends2).  Measured
+// (bf16 C, us): 64 x 64 tiles 256 x 4096 x 4096 13.6, 512 x 4096 x 4096 19.9, 2048^3 21.1;
+// 128 x 64 512 x 4096 x 1024 8.2, x 4096 18.0; 128 x 128 2048^3 15.3, 1024 x 4096 x 4096
+// 23.9; 256 x 256 4096 x 4096 x 1024 25.1, 4096^3 63.7.
+I8GemmPlan plan_tiles(int64_t M, int64_t N, int64_t K, int64_t room, double &us)
+{
+    static const struct { int kid, bm, bn, threads; double step, ends, step2, ends2; } kTiles[4] = {
+        {KID_I8_S, 64, 64, 256, 0.30, 2.2, 0.517, 1.4}, {KID_I8_N, 128, 64, 512, 0.43, 2.5, 0, 0},
+        {KID_I8_M, 128, 128, 512, 0.565, 3.1, 0, 0}, {KID_I8_L, 256, 256, 512, 1.62, 10.2, 0, 0}};
+    I8GemmPlan p;
+    const int64_t nk = ceil_div(K, F8_BLOCK);
+    const double bytes_us = 2.2 + ((double)(M + N) * (double)K + 3.0 * (double)M * (double)N) / 5.0e6;
+    for (const auto &t : kTiles) {
+        const int64_t tm = ceil_div(M, t.bm), tn = ceil_div(N, t.bn);
+        for (int64_t splits = 1; splits <= 16; splits *= 2) {
+            const int64_t part = ceil_div(nk, splits), all = tm * tn * splits;
+            if (splits > 1 && (part < 4 || (splits - 1) * part >= nk || all > 512 ||
+                               splits * M * N * 4 > std::min(room, kMaxJoin)))
+                break;
+            const double one = (double)part * t.step + t.ends, two = (double)part * t.step2 + t.ends2;
+            const double rounds = t.step2 > 0 ? (double)(all / 512) * two + (all % 512 > 256 ? two : all % 512 > 0 ? one : 0.0)
+                                              : (double)ceil_div(all, 256) * one;
+            const int64_t bytes = splits > 1 ? splits * M * N * 4 : 0;
+            const double e = 2.0 + std::max(rounds, bytes_us) + (splits > 1 ? join_us(bytes) : 0.0);
+            if (p.kid == KID_I8_NONE || e < us) {
+                us = e;
+                p = I8GemmPlan{t.kid, tm, tn, splits, bytes, 0, t.threads};
+            }
+        }
+    }
+    return p;
+}
+
+// Up to 16 rows: 16 columns per workgroup, 32 where that still leaves two workgroups to
+// each CU (16 x 16384 x 4096 20.0 / 15.7 us, 8 x 8192 x 8192 16.2 / 19.4), k split where
+// few workgroups go through a long k (1 x 1024 x 16384 11.9 us, in 8 parts 6.8 and the join).
+int skinny_cols(int64_t N) { return N < 16384 ? 16 : 32; }
+
+I8GemmPlan plan_skinny(int64_t M, int64_t N, int64_t K, int64_t room)
+{
+    I8GemmPlan p;
+    const int64_t nk = ceil_div(K, F8_BLOCK), tn = ceil_div(N, skinny_cols(N));
+    double us = 0.0;
+    for (int64_t splits = 1; splits <= 16; splits *= 2) {
+        const int64_t part = ceil_div(nk, splits), bytes = splits > 1 ? splits * M * N * 4 : 0;
+        if (splits > 1 && (part < 8 || (splits - 1) * part >= nk || tn * splits > 512 || bytes > std::min(room, kMaxJoin)))
+            break;
+        const double e = std::max(1.6 + 0.52 * (double)ceil_div(part, 8), (double)N * (double)K / 4.6e6) +
+                         (splits > 1 ? join_us(bytes) : 0.0);
+        if (splits == 1 || e < us) {
+            us = e;
+            p = I8GemmPlan{KID_I8_SKINNY, 1, tn, splits, bytes, 0, 512};
+        }
+    }
+    return p;
+}
 
 }  // namespace
 
-I8GemmPlan i8_gemm_plan(int64_t M, int64_t N, int64_t, bool, int64_t, bool)
+// Operands at other alignments go through the registers of the 64 x 64 tile, or, where that
+// takes longer, are first laid out anew in the workspace with rows of whole lines.
+I8GemmPlan i8_gemm_plan(int64_t M, int64_t N, int64_t K, bool aligned, int64_t room, bool may_pack)
 {
+    if (M <= 16)
+        return plan_skinny(M, N, K, room);
+    double us = 0.0;
+    if (aligned && N > 1)  // (a single row of B has no distance to the next)
+        return plan_tiles(M, N, K, room, us);
     I8GemmPlan p;
     p.kid = KID_I8_ANY;
     p.tiles_m = ceil_div(M, GS::BM);
     p.tiles_n = ceil_div(N, GS::BN);
     p.threads = GS::NT;
+    const int64_t ld = f8_packed_ld(K);
+    if (may_pack && N > 1 && M <= F8_MAX_PACKED / ld && N <= F8_MAX_PACKED / ld && (M + N) * ld <= room) {
+        const int64_t pack = (M + N) * ld;
+        const I8GemmPlan q = plan_tiles(M, N, K, room - pack, us);
+        const double any = 2.5 + (double)ceil_div(K, F8_BLOCK) * std::max(0.62, (double)p.tiles_m * (double)p.tiles_n * 0.9e-3);
+        if (us + 4.0 + (double)pack * 0.35e-6 < any) {
+            p = q;
+            p.bytes += pack;
+            p.pack = pack;
+        }
+    }
     return p;
 }
 
@@ -107,7 +208,43 @@ hipError_t launch_i8_gemm(I8GemmArgs a, const I8GemmPlan &p, hipStream_t s)
 {
     a.tiles_m = (int)p.tiles_m;
     a.tiles_n = (int)p.tiles_n;
-    i8_tile_kernel<GS><<<(unsigned)(p.tiles_m * p.tiles_n), GS::NT, 0, s>>>(a);
+    if (p.kid >= KID_I8_S && !p.pack && std::max(a.lda, a.ldb) > F8_MAX_LD)
+        return hipErrorInvalidValue;  // (the pipelined kernels' offsets have 32 bits)
+    if (p.pack) {
+        F8GemmArgs f{};
+        f.A = a.A;
+        f.B = a.B;
+        f.lda = a.lda;
+        f.ldb = a.ldb;
+        f.M = a.M;
+        f.N = a.N;
+        f.K = a.K;
+        uint8_t *to = reinterpret_cast<uint8_t *>(a.ws);
+        const hipError_t e = launch_f8_pack(f, to, s);
+        if (e != hipSuccess)
+            return e;
+        const int64_t ld = f8_packed_ld(a.K);
+        a.A = to;
+        a.B = to + (int64_t)a.M * ld;
+        a.lda = a.ldb = ld;
+        a.ws = reinterpret_cast<int *>(to + p.pack);
+    }
+    if (p.splits == 1)
+        a.ws = nullptr;
+    const int splits = (int)p.splits;
+    a.kb_split = (int)ceil_div(ceil_div(a.K, F8_BLOCK), splits);
+    hipError_t e = hipSuccess;
+    if (p.kid == KID_I8_SKINNY) {
+        e = launch_i8_skinny(a, skinny_cols(a.N), splits, s);
+    } else if (p.kid == KID_I8_ANY) {
+        i8_tile_kernel<GS><<<(unsigned)(p.tiles_m * p.tiles_n), GS::NT, 0, s>>>(a);
+        e = hipGetLastError();
+    } else {
+        e = launch_i8_tile(a, p.kid, splits, s);
+    }
+    if (e != hipSuccess || splits == 1)
+        return e;
+    i8_join_kernel<<<(unsigned)std::min<int64_t>(ceil_div((int64_t)a.M * ceil_div(a.N, 8), 256), 2048), 256, 0, s>>>(a, splits);
     return hipGetLastError();
 }
 

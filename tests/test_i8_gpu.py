@@ -104,6 +104,22 @@ def test_gemm_larger_and_the_same_with_any_workspace(M, N, K):
     run_gemm(M, N, K, ct="f32", pad=3, offset=1)
 
 
+# (M, N, K, kernel, splits or 1): every kernel with k that ends within 16 bytes, within a k-block and
+# on its end, one and two k-blocks, splits of unequal length, and edges in both directions
+KERNELS = [(16, 1000, 16384, 90, 4), (3, 500, 12345, 90, 8), (9, 17000, 200, 90, 1), (200, 200, 3000, 92, 4),
+           (33, 1000, 8205, 92, 8), (700, 700, 128, 92, 1), (1000, 999, 129, 92, 1), (510, 4000, 4097, 93, 1),
+           (500, 4090, 4080, 93, 1), (1000, 4000, 2049, 94, 1), (1010, 4090, 1920, 94, 1), (2047, 8100, 1000, 95, 1),
+           (2040, 8190, 1040, 95, 1), (8100, 8000, 144, 95, 1)]
+
+
+@pytest.mark.parametrize("M,N,K,kid,splits", KERNELS)
+def test_gemm_every_kernel(M, N, K, kid, splits):
+    plan = lib.sgemm_i8_gemm_plan(M, N, K, 1)
+    assert plan[1] == kid and (plan[4] > 1) == (splits > 1), plan
+    run_gemm(M, N, K)
+    run_gemm(M, N, K, ct="f32", beta=-0.5, ldc_pad=5)
+
+
 @pytest.mark.parametrize("M,N", [(1, 40), (20, 70), (70, 130), (300, 260)])
 def test_gemm_largest_sums(M, N):
     # -128 times -128 in every place of the longest k: 131071 * 2^14, 16384 below 2^31

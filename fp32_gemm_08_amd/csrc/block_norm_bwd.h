@@ -66,6 +66,40 @@ __device__ __forceinline__ void weights8(const void *W, int64_t at, int w_f32, i
     }
 }
 
+// A workgroup's sums of its columns: of its rows of lanes in order, through `sums`.
+template <int NT, int L, int V>
+__device__ __forceinline__ void block_norm_put_sums(float *out, float *sums, int lane, int own, int cols,
+                                                    const float (*v)[8])
+{
+    constexpr int ROWS = NT / L;
+    if constexpr (ROWS == 1) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (8 * (lane + L * i) < cols)
+                row_store8(out, 8 * (lane + L * i), cols, v[i]);
+    } else {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                sums[(own * 8 + j) * (V * L) + L * i + lane] = v[i][j];
+        __syncthreads();
+        for (int c = threadIdx.x; c < cols; c += NT) {
+            float s = 0.0f;
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r)
+                s += sums[(r * 8 + c % 8) * (V * L) + c / 8];
+            out[c] = s;
+        }
+    }
+}
+
+// What a work-item holds of a row: V pieces of 8 consecutive columns.  Its sums of dw and
+// t, and with one piece also w and gate * w_post, stay in registers: with these, two rows
+// of 16-bit values and the working values one piece fits the 128 registers of 16
+// wavefronts per CU.  More pieces read the weights again for every row, from the L2.
+// dw_post, which changes once per row of the gate, is kept in the LDS.
 // AHEAD: the next row's values are requested before this row's are used.  SEVERAL: the
 // gate has more rows than one.
 template <typename T, int NT, int L, int V, bool AHEAD, bool KEPT, bool SEVERAL>
@@ -74,34 +108,42 @@ __global__ __launch_bounds__(NT) void block_norm_bwd_kernel(BlockNormBwdArgs g)
     typedef typename Elt<T>::Raw Raw;
     typedef Source<T, KEPT> Src;
     constexpr int ROWS = NT / L;
+    constexpr bool HOLD = V == 1;
     __shared__ float slot[4][NT / 64];
-    __shared__ float sums[ROWS > 1 ? NT * 8 * V : 1];
-    const int lane = threadIdx.x % L, own = threadIdx.x / L;
+    __shared__ float sums[SEVERAL || ROWS > 1 ? NT * 8 * V : 1];
+    const int lane = threadIdx.x % L, own = ROWS == 1 ? 0 : threadIdx.x / L;
     const bool read_o = g.O != nullptr, out_o = g.DO || g.DWP || g.DG;
     const int64_t walker = (int64_t)blockIdx.x * ROWS + own, r0 = walker * g.chunk;
     const int64_t r1 = min<int64_t>(g.rows, r0 + g.chunk);
+    auto col = [&](int i) { return 8 * (lane + L * i); };
+    auto held = [&](int i, int j) -> float & { return sums[(j * V + i) * NT + threadIdx.x]; };
 
-    float w[V][8], wp[V][8], gate[V][8], dw[V][8], t[V][8], dwp[SEVERAL ? V : 1][8];
     int gr = SEVERAL ? (int)((uint32_t)min<int64_t>(r0, g.rows - 1) / (uint32_t)g.gate_rows) : 0;  // the gate's row
     int64_t gate_end = SEVERAL ? (int64_t)(gr + 1) * g.gate_rows : g.rows;
-    auto load_gate = [&] {
+    auto gate_weight = [&](int i, float (&v)[8]) {  // gate * w_post
+        float wp[8];
+        weights8<T>(g.G, gr * g.ldg, g.w_f32, col(i), g.cols, v);
+        weights8<T>(g.WP, 0, g.w_f32, col(i), g.cols, wp);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            weights8<T>(g.G, gr * g.ldg, g.w_f32, 8 * (lane + L * i), g.cols, gate[i]);
+        for (int j = 0; j < 8; ++j)
+            v[j] *= wp[j];
     };
-    load_gate();
+    float hw[HOLD ? V : 1][8], hgw[HOLD ? V : 1][8], dw[V][8], t[V][8];
+    if constexpr (HOLD) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int c = 8 * (lane + L * i);
-        weights8<T>(g.W, 0, g.w_f32, c, g.cols, w[i]);
-        weights8<T>(g.WP, 0, g.w_f32, c, g.cols, wp[i]);
+        for (int i = 0; i < V; ++i) {
+            weights8<T>(g.W, 0, g.w_f32, col(i), g.cols, hw[i]);
+            gate_weight(i, hgw[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             dw[i][j] = t[i][j] = 0.0f;
             if (SEVERAL)
-                dwp[i][j] = 0.0f;
+                held(i, j) = 0.0f;
         }
-    }
     struct Row {
         Raw dy[V], dh[V];
         typename Src::Raw h[V], o[V];
@@ -110,7 +152,7 @@ __global__ __launch_bounds__(NT) void block_norm_bwd_kernel(BlockNormBwdArgs g)
     auto request = [&](int64_t row, Row &to) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = 8 * (lane + L * i);
+            const int c = col(i);
             if (g.DY) {
                 to.dy[i] = row_raw8<true>(static_cast<const T *>(g.DY) + row * g.lddy, c, g.cols);
                 Src::load(to.h[i], g.H, g.ldh, g.SH, g.ldsh, row, c, g.cols);
@@ -139,12 +181,14 @@ __global__ __launch_bounds__(NT) void block_norm_bwd_kernel(BlockNormBwdArgs g)
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                float h[8];
+                float h[8], w[8];
                 Src::values(a.h[i], h);
+                if constexpr (!HOLD)
+                    weights8<T>(g.W, 0, g.w_f32, col(i), g.cols, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float dy = (float)a.dy[i][j], n = h[j] * a.rstd;
-                    sum = fmaf(dy * w[i][j], n, sum);
+                    sum = fmaf(dy * (HOLD ? hw[HOLD ? i : 0][j] : w[j]), n, sum);
                     dw[i][j] = fmaf(dy, n, dw[i][j]);
                 }
             }
@@ -153,44 +197,48 @@ __global__ __launch_bounds__(NT) void block_norm_bwd_kernel(BlockNormBwdArgs g)
         float p[V][8], sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = 8 * (lane + L * i);
-            float h[8], o[8], dx[8];
+            float h[8], o[8], dx[8], w[8], gw[8];
             if (g.DY)
                 Src::values(a.h[i], h);
             if (read_o)
                 Src::values(a.o[i], o);
+            if constexpr (!HOLD) {
+                if (g.DY)
+                    weights8<T>(g.W, 0, g.w_f32, col(i), g.cols, w);
+                if (out_o)
+                    gate_weight(i, gw);
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                float d = g.DY ? a.rstd * ((float)a.dy[i][j] * w[i][j] - h[j] * a.rstd * mean) : 0.0f;
+                float d = g.DY ? a.rstd * ((float)a.dy[i][j] * (HOLD ? hw[HOLD ? i : 0][j] : w[j]) - h[j] * a.rstd * mean) : 0.0f;
                 if (g.DH)
                     d += (float)a.dh[i][j];
                 dx[j] = g.alpha * d;
-                p[i][j] = gate[i][j] * d * wp[i][j];
+                if (out_o)
+                    p[i][j] = d * (HOLD ? hgw[HOLD ? i : 0][j] : gw[j]);
                 if (read_o) {
                     const float m = o[j] * a.rstd_post;
                     sum = fmaf(p[i][j], m, sum);
                     t[i][j] = fmaf(d, m, t[i][j]);
                 }
             }
-            if (g.DX && c < g.cols)
-                row_store8(static_cast<T *>(g.DX) + row * g.lddx, c, g.cols, dx);
+            if (g.DX && col(i) < g.cols)
+                row_store8(static_cast<T *>(g.DX) + row * g.lddx, col(i), g.cols, dx);
         }
-        if (out_o) {
+        if (g.DO) {
             mean = g.WP ? row_sum<NT, L>(sum, slot[2 + turn]) / (float)g.cols : 0.0f;
-            if (g.DO) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int c = 8 * (lane + L * i);
-                    if (c >= g.cols)
-                        continue;
+            for (int i = 0; i < V; ++i) {
+                if (col(i) >= g.cols)
+                    continue;
+                if (g.WP) {
                     float o[8];
-                    if (read_o)
-                        Src::values(a.o[i], o);
+                    Src::values(a.o[i], o);
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        p[i][j] = g.WP ? a.rstd_post * (p[i][j] - o[j] * a.rstd_post * mean) : p[i][j];
-                    row_store8(static_cast<T *>(g.DO) + row * g.lddo, c, g.cols, p[i]);
+                        p[i][j] = a.rstd_post * (p[i][j] - o[j] * a.rstd_post * mean);
                 }
+                row_store8(static_cast<T *>(g.DO) + row * g.lddo, col(i), g.cols, p[i]);
             }
         }
         if constexpr (SEVERAL) {
@@ -202,15 +250,19 @@ __global__ __launch_bounds__(NT) void block_norm_bwd_kernel(BlockNormBwdArgs g)
                                      : g.ws + (2 * (int64_t)g.groups + 2 * walker + (first > r0)) * g.cols;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const int c = 8 * (lane + L * i);
+                    float v[8];
+                    weights8<T>(g.G, gr * g.ldg, g.w_f32, col(i), g.cols, v);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        dwp[i][j] = fmaf(gate[i][j], t[i][j], dwp[i][j]);
-                        if (whole)
-                            t[i][j] *= wp[i][j];
+                    for (int j = 0; j < 8; ++j)
+                        held(i, j) = fmaf(v[j], t[i][j], held(i, j));
+                    if (out && whole) {
+                        weights8<T>(g.WP, 0, g.w_f32, col(i), g.cols, v);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            t[i][j] *= v[j];
                     }
-                    if (out && c < g.cols)
-                        row_store8(out, c, g.cols, t[i]);
+                    if (out && col(i) < g.cols)
+                        row_store8(out, col(i), g.cols, t[i]);
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         t[i][j] = 0.0f;
@@ -218,41 +270,184 @@ __global__ __launch_bounds__(NT) void block_norm_bwd_kernel(BlockNormBwdArgs g)
                 if (row + 1 < r1) {
                     ++gr;
                     gate_end += g.gate_rows;
-                    load_gate();
+                    if constexpr (HOLD) {
+#pragma unroll
+                        for (int i = 0; i < V; ++i)
+                            gate_weight(i, hgw[i]);
+                    }
                 }
             }
         }
     }
-    // the workgroup's sums: of dy n, and of d m or gate d m
+    // the workgroup's sums: of d m or gate d m, and of dy n
+    if constexpr (SEVERAL) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        if (!(k == 0 ? g.DW : SEVERAL ? g.DWP : g.DWP || g.DG ? g.ws : nullptr))
-            continue;
-        float *out = g.ws + ((int64_t)k * g.groups + blockIdx.x) * g.cols;
-        if constexpr (ROWS == 1) {
+        for (int i = 0; i < V; ++i)
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int c = 8 * (lane + L * i);
-                if (c < g.cols)
-                    row_store8(out, c, g.cols, k == 0 ? dw[i] : SEVERAL ? dwp[i] : t[i]);
-            }
-        } else {
-            __syncthreads();
+            for (int j = 0; j < 8; ++j)
+                t[i][j] = held(i, j);
+    }
+    if (g.DW)
+        block_norm_put_sums<NT, L, V>(g.ws + (int64_t)blockIdx.x * g.cols, sums, lane, own, g.cols, dw);
+    if (SEVERAL ? g.DWP != nullptr : g.DWP || g.DG)
+        block_norm_put_sums<NT, L, V>(g.ws + ((int64_t)g.groups + blockIdx.x) * g.cols, sums, lane, own, g.cols, t);
+}
+
+// The same for whole pieces (cols a multiple of 8) with every operand and DX and DO there,
+// one piece a work-item: no conditions in the loop, the next row's values requested as soon
+// as this row's are converted, and n, g, m and p kept from one pass over the row to the next.
+template <typename T, int NT, int L, bool KEPT, bool SEVERAL>
+__global__ __launch_bounds__(NT) void block_norm_bwd_whole_kernel(BlockNormBwdArgs g)
+{
+    typedef typename Elt<T>::Raw Raw;
+    typedef Source<T, KEPT> Src;
+    constexpr int ROWS = NT / L;
+    __shared__ float slot[4][NT / 64];
+    __shared__ float sums[SEVERAL || ROWS > 1 ? NT * 8 : 1];
+    const int lane = threadIdx.x % L, own = ROWS == 1 ? 0 : threadIdx.x / L;
+    const int64_t walker = (int64_t)blockIdx.x * ROWS + own, r0 = walker * g.chunk;
+    const int64_t r1 = min<int64_t>(g.rows, r0 + g.chunk);
+    const bool live = 8 * lane < g.cols;
+    const int c = live ? 8 * lane : 0;      // (work-items past the row's end take its first piece, and add zeros)
+    auto held = [&](int j) -> float & { return sums[j * NT + threadIdx.x]; };
+
+    int gr = SEVERAL ? (int)((uint32_t)min<int64_t>(r0, g.rows - 1) / (uint32_t)g.gate_rows) : 0;  // the gate's row
+    int64_t gate_end = SEVERAL ? (int64_t)(gr + 1) * g.gate_rows : g.rows;
+    float w[8], gw[8], dw[8], t[8];
+    auto gate_weight = [&] {  // gate * w_post
+        float wp[8];
+        weights8<T>(g.G, gr * g.ldg, g.w_f32, c, g.cols, gw);
+        weights8<T>(g.WP, 0, g.w_f32, c, g.cols, wp);
 #pragma unroll
-            for (int i = 0; i < V; ++i)
+        for (int j = 0; j < 8; ++j)
+            gw[j] *= wp[j];
+    };
+    weights8<T>(g.W, 0, g.w_f32, c, g.cols, w);
+    gate_weight();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        dw[j] = t[j] = 0.0f;
+        if (SEVERAL)
+            held(j) = 0.0f;
+    }
+    struct Row {
+        Raw dy, dh;
+        typename Src::Raw h, o;
+        float rstd, rstd_post;
+    } b;
+    auto request = [&](int64_t row) {
+        b.dy = Elt<T>::template raw8<true>(static_cast<const T *>(g.DY) + row * g.lddy + c);
+        Src::load(b.h, g.H, g.ldh, g.SH, g.ldsh, row, c, c + 8);
+        b.dh = Elt<T>::template raw8<true>(static_cast<const T *>(g.DH) + row * g.lddh + c);
+        Src::load(b.o, g.O, g.ldo, g.SO, g.ldso, row, c, c + 8);
+        b.rstd = g.rstd[row];
+        b.rstd_post = g.rstd_post[row];
+    };
+    if (r0 < r1)
+        request(r0);
+    const float per_col = 1.0f / (float)g.cols;
+    int turn = 0;
+    for (int64_t row = r0; row < r1; ++row, turn ^= 1) {
+        const float rstd = b.rstd, rp = b.rstd_post;
+        float n[8], gy[8], m[8], p[8], dh[8], sum = 0.0f;
+        Src::values(b.h, n);
+        Src::values(b.o, m);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float dy = (float)b.dy[j];
+            n[j] *= rstd;
+            m[j] *= rp;
+            dh[j] = (float)b.dh[j];
+            gy[j] = dy * w[j];
+            sum = fmaf(gy[j], n[j], sum);
+            dw[j] = fmaf(dy, n[j], dw[j]);
+        }
+        if (row + 1 < r1)
+            request(row + 1);
+        const float mean = row_sum<NT, L>(live ? sum : 0.0f, slot[turn]) * per_col;
+        float dx[8];
+        sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float d = fmaf(rstd, fmaf(-mean, n[j], gy[j]), dh[j]);
+            dx[j] = g.alpha * d;
+            p[j] = d * gw[j];
+            sum = fmaf(p[j], m[j], sum);
+            t[j] = fmaf(d, m[j], t[j]);
+        }
+        if (live)
+            Elt<T>::store8(static_cast<T *>(g.DX) + row * g.lddx + c, dx);
+        const float back = row_sum<NT, L>(live ? sum : 0.0f, slot[2 + turn]) * per_col * rp;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            p[j] = fmaf(rp, p[j], -back * m[j]);
+        if (live)
+            Elt<T>::store8(static_cast<T *>(g.DO) + row * g.lddo + c, p);
+        if constexpr (SEVERAL) {
+            if (row + 1 == r1 || row + 1 == gate_end) {
+                const int64_t first = gate_end - g.gate_rows;
+                const bool whole = first >= r0 && (row + 1 == gate_end || row + 1 == g.rows);
+                float *out = !g.DG ? nullptr
+                             : whole ? g.DG + gr * g.lddg
+                                     : g.ws + (2 * (int64_t)g.groups + 2 * walker + (first > r0)) * g.cols;
+                float v[8];
+                weights8<T>(g.G, gr * g.ldg, g.w_f32, c, g.cols, v);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    sums[(own * 8 + j) * (V * L) + L * i + lane] = k == 0 ? dw[i][j] : SEVERAL ? dwp[i][j] : t[i][j];
-            __syncthreads();
-            for (int c = threadIdx.x; c < g.cols; c += NT) {
-                float s = 0.0f;
+                    held(j) = fmaf(v[j], t[j], held(j));
+                if (out && whole) {
+                    weights8<T>(g.WP, 0, g.w_f32, c, g.cols, v);
 #pragma unroll
-                for (int r = 0; r < ROWS; ++r)
-                    s += sums[(r * 8 + c % 8) * (V * L) + c / 8];
-                out[c] = s;
+                    for (int j = 0; j < 8; ++j)
+                        t[j] *= v[j];
+                }
+                if (out && live)
+                    Elt<float>::store8(out + c, t);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    t[j] = 0.0f;
+                if (row + 1 < r1) {
+                    ++gr;
+                    gate_end += g.gate_rows;
+                    gate_weight();
+                }
             }
         }
     }
+    if constexpr (SEVERAL) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            t[j] = held(j);
+    }
+    if (g.DW)
+        block_norm_put_sums<NT, L, 1>(g.ws + (int64_t)blockIdx.x * g.cols, sums, lane, own, g.cols, &dw);
+    if (SEVERAL ? g.DWP != nullptr : g.DWP || g.DG)
+        block_norm_put_sums<NT, L, 1>(g.ws + ((int64_t)g.groups + blockIdx.x) * g.cols, sums, lane, own, g.cols, &t);
+}
+
+// Work-items of a workgroup and of a row, and pieces per work-item: one piece up to 8192
+// columns.
+template <typename T, typename F>
+void bwd_by_cols(int cols, F f)
+{
+    if (cols <= 128)
+        f.template run<T, 256, 16, 1>();
+    else if (cols <= 256)
+        f.template run<T, 256, 32, 1>();
+    else if (cols <= 512)
+        f.template run<T, 256, 64, 1>();
+    else if (cols <= 1024)
+        f.template run<T, 128, 128, 1>();
+    else if (cols <= 2048)
+        f.template run<T, 256, 256, 1>();
+    else if (cols <= 4096)
+        f.template run<T, 512, 512, 1>();
+    else if (cols <= 8192)
+        f.template run<T, 512, 512, 2>();
+    else if (cols <= 16384)
+        f.template run<T, 512, 512, 4>();
+    else
+        f.template run<T, 1024, 1024, 4>();
 }
 
 struct Bwd {
@@ -261,7 +456,14 @@ struct Bwd {
     hipStream_t s;
     template <typename T, int NT, int L, int V, bool KEPT, bool SEVERAL> void go()
     {
-        block_norm_bwd_kernel<T, NT, L, V, false, KEPT, SEVERAL><<<(unsigned)a.groups, NT, 0, s>>>(a);
+        if constexpr (V == 1) {
+            if (a.cols % 8 == 0 && a.DY && a.DH && a.DX && a.DO && a.WP) {
+                block_norm_bwd_whole_kernel<T, NT, L, KEPT, SEVERAL><<<(unsigned)a.groups, NT, 0, s>>>(a);
+                return;
+            }
+        }
+        constexpr bool AHEAD = V == 2 && sizeof(T) == 2;
+        block_norm_bwd_kernel<T, NT, L, V, AHEAD, KEPT, SEVERAL><<<(unsigned)a.groups, NT, 0, s>>>(a);
     }
     template <typename T, int NT, int L, int V> void run()
     {

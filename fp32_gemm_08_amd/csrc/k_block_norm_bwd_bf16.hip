@@ -5,7 +5,7 @@ namespace sgemm {
 
 template <> void launch_block_norm_bwd_rows<__bf16>(const BlockNormBwdArgs &a, bool kept, bool several, hipStream_t s)
 {
-    by_cols<__bf16>(a.cols, Bwd{a, kept, several, s});
+    bwd_by_cols<__bf16>(a.cols, Bwd{a, kept, several, s});
 }
 
 }  // namespace sgemm

@@ -83,13 +83,13 @@ __global__ __launch_bounds__(1024) void block_norm_sums_kernel(BlockNormBwdArgs 
     }
 }
 
-// Workgroups of 4 to 8 wavefronts per CU, as in the other norm's backward pass.
+// 8 wavefronts per CU.
 struct Walkers {
     int64_t rows;
     BlockNormSums *out;
     template <typename T, int NT, int L, int V> void run()
     {
-        constexpr int64_t ROWS = NT / L, MOST = NT >= 512 ? 256 : V == 1 ? 768 : 512;
+        constexpr int64_t ROWS = NT / L, MOST = std::max(256 * 512 / NT, 256);
         const int64_t all = MOST * ROWS;
         out->chunk = std::max<int64_t>(1, ceil_div(rows, all));
         out->groups = ceil_div(ceil_div(rows, out->chunk), ROWS);
@@ -104,7 +104,7 @@ BlockNormSums block_norm_sums(int64_t rows, int64_t cols, int64_t gate_rows)
     BlockNormSums n;
     if (rows <= 0 || cols <= 0)
         return n;
-    by_cols<float>((int)cols, Walkers{rows, &n});
+    bwd_by_cols<float>((int)cols, Walkers{rows, &n});
     n.several = gate_rows > 0 && gate_rows < rows;
     n.parts = 2 * n.groups + (n.several ? 2 * n.walkers : 0);
     return n;

@@ -7,9 +7,8 @@
 //     dw_post = sum over gates of gate * t         dgate = w_post * t
 //
 // so one sum t serves both of the last.  A walker (a workgroup, or the 16 to 64 lanes
-// that hold a row) takes consecutive rows and keeps its columns' sums in registers; a
-// second kernel adds what the walkers left, in a fixed order.  Consecutive rows, since
-// the scales of 32 consecutive rows' blocks share a line.
+// that hold a row) takes rows one after another and keeps its columns' sums; a second kernel
+// adds what the workgroups left, in a fixed order.
 #pragma once
 #include "norm_internal.h"
 #include "norm_rows.h"
@@ -66,6 +65,36 @@ __device__ __forceinline__ void weights8(const void *W, int64_t at, int w_f32, i
     }
 }
 
+// The rows of a walker.  One gate a walker: `team` workgroups share a gate's rows and take
+// them in turn, so that all walkers of a gate are at neighbouring rows at a time (rows in
+// runs of a walker's own took 154 instead of 138 us, 16384 x 4096 bf16), and workgroups of
+// one XCD at the nearest, since the scales of 32 consecutive rows share a line.  SEVERAL:
+// `chunk` consecutive rows.
+template <bool SEVERAL, int ROWS> struct BlockNormWalk {
+    int group;              // of the workgroup, in the order of the sums
+    int gate;               // the first row's
+    int64_t walker, first, end;
+    int step;
+    __device__ __forceinline__ BlockNormWalk(const BlockNormBwdArgs &g, int own)
+    {
+        const int n = g.groups;
+        group = n % 8 == 0 ? (int)(blockIdx.x % 8) * (n / 8) + (int)(blockIdx.x / 8) : (int)blockIdx.x;
+        walker = (int64_t)group * ROWS + own;
+        if constexpr (SEVERAL) {
+            first = walker * g.chunk;
+            end = min<int64_t>(g.rows, first + g.chunk);
+            step = 1;
+            gate = (int)((uint32_t)min<int64_t>(first, g.rows - 1) / (uint32_t)g.gate_rows);
+        } else {
+            gate = group / g.team;
+            const int64_t begin = (int64_t)gate * g.gate_rows;
+            first = begin + (int64_t)(group - gate * g.team) * ROWS + own;
+            end = min<int64_t>(g.rows, begin + g.gate_rows);
+            step = g.team * ROWS;
+        }
+    }
+};
+
 // A workgroup's sums of its columns: of its rows of lanes in order, through `sums`.
 template <int NT, int L, int V>
 __device__ __forceinline__ void block_norm_put_sums(float *out, float *sums, int lane, int own, int cols,
@@ -95,31 +124,32 @@ __device__ __forceinline__ void block_norm_put_sums(float *out, float *sums, int
     }
 }
 
-// What a work-item holds of a row: V pieces of 8 consecutive columns.  Its sums of dw and
-// t, and with one piece also w and gate * w_post, stay in registers: with these, two rows
-// of 16-bit values and the working values one piece fits the 128 registers of 16
-// wavefronts per CU.  More pieces read the weights again for every row, from the L2.
-// dw_post, which changes once per row of the gate, is kept in the LDS.
-// AHEAD: the next row's values are requested before this row's are used.  SEVERAL: the
-// gate has more rows than one.
+// What a work-item holds of a row: V pieces of 8 consecutive columns.  With one piece its
+// sums of dw and t, w and gate * w_post stay in registers; with more the weights are read
+// again for every row, from the L2, and with two the sums are in the LDS (1024 work-items
+// have 128 registers each).  AHEAD: the next row's values are requested before this row's
+// are used.  SEVERAL: a walker's rows may have several gates; dw_post, which then changes
+// once per gate, is kept in the LDS, or (two pieces) in the workgroup's place in the
+// workspace, by the work-item that has its columns.
 template <typename T, int NT, int L, int V, bool AHEAD, bool KEPT, bool SEVERAL>
 __global__ __launch_bounds__(NT) void block_norm_bwd_kernel(BlockNormBwdArgs g)
 {
     typedef typename Elt<T>::Raw Raw;
     typedef Source<T, KEPT> Src;
     constexpr int ROWS = NT / L;
-    constexpr bool HOLD = V == 1;
+    constexpr bool HOLD = V == 1, FAR = V == 2;
     __shared__ float slot[4][NT / 64];
-    __shared__ float sums[SEVERAL || ROWS > 1 ? NT * 8 * V : 1];
+    __shared__ float sums[FAR ? 2 * NT * 8 * V : SEVERAL || ROWS > 1 ? NT * 8 * V : 1];
     const int lane = threadIdx.x % L, own = ROWS == 1 ? 0 : threadIdx.x / L;
     const bool read_o = g.O != nullptr, out_o = g.DO || g.DWP || g.DG;
-    const int64_t walker = (int64_t)blockIdx.x * ROWS + own, r0 = walker * g.chunk;
-    const int64_t r1 = min<int64_t>(g.rows, r0 + g.chunk);
+    const BlockNormWalk<SEVERAL, ROWS> walk(g, own);
+    const int64_t walker = walk.walker, r0 = walk.first, r1 = walk.end;
     auto col = [&](int i) { return 8 * (lane + L * i); };
     auto held = [&](int i, int j) -> float & { return sums[(j * V + i) * NT + threadIdx.x]; };
+    float *place = g.ws + ((int64_t)g.groups + walk.group) * g.cols;  // (two pieces) of dw_post
 
-    int gr = SEVERAL ? (int)((uint32_t)min<int64_t>(r0, g.rows - 1) / (uint32_t)g.gate_rows) : 0;  // the gate's row
-    int64_t gate_end = SEVERAL ? (int64_t)(gr + 1) * g.gate_rows : g.rows;
+    int gr = walk.gate;
+    int64_t gate_end = (int64_t)(gr + 1) * g.gate_rows;
     auto gate_weight = [&](int i, float (&v)[8]) {  // gate * w_post
         float wp[8];
         weights8<T>(g.G, gr * g.ldg, g.w_f32, col(i), g.cols, v);
@@ -128,22 +158,6 @@ __global__ __launch_bounds__(NT) void block_norm_bwd_kernel(BlockNormBwdArgs g)
         for (int j = 0; j < 8; ++j)
             v[j] *= wp[j];
     };
-    float hw[HOLD ? V : 1][8], hgw[HOLD ? V : 1][8], dw[V][8], t[V][8];
-    if constexpr (HOLD) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            weights8<T>(g.W, 0, g.w_f32, col(i), g.cols, hw[i]);
-            gate_weight(i, hgw[i]);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            dw[i][j] = t[i][j] = 0.0f;
-            if (SEVERAL)
-                held(i, j) = 0.0f;
-        }
     struct Row {
         Raw dy[V], dh[V];
         typename Src::Raw h[V], o[V];
@@ -167,12 +181,35 @@ __global__ __launch_bounds__(NT) void block_norm_bwd_kernel(BlockNormBwdArgs g)
     };
     if (AHEAD && r0 < r1)
         request(r0, b);
+    float hw[HOLD ? V : 1][8], hgw[HOLD ? V : 1][8], rdw[FAR ? 1 : V][8], rt[FAR ? 1 : V][8];
+    auto dw = [&](int i, int j) -> float & { return FAR ? sums[(j * V + i) * NT + threadIdx.x] : rdw[FAR ? 0 : i][j]; };
+    auto t = [&](int i, int j) -> float & { return FAR ? sums[((8 + j) * V + i) * NT + threadIdx.x] : rt[FAR ? 0 : i][j]; };
+    if constexpr (HOLD) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            weights8<T>(g.W, 0, g.w_f32, col(i), g.cols, hw[i]);
+            gate_weight(i, hgw[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            dw(i, j) = t(i, j) = 0.0f;
+            if (SEVERAL && !FAR)
+                held(i, j) = 0.0f;
+        }
+        if (SEVERAL && FAR && g.DWP && col(i) < g.cols) {
+            const float zero[8] = {};
+            row_store8(place, col(i), g.cols, zero);
+        }
+    }
     int turn = 0;
-    for (int64_t row = r0; row < r1; ++row, turn ^= 1) {
+    for (int64_t row = r0; row < r1; row += walk.step, turn ^= 1) {
         if constexpr (AHEAD) {
             a = b;
-            if (row + 1 < r1)
-                request(row + 1, b);
+            if (row + walk.step < r1)
+                request(row + walk.step, b);
         } else {
             request(row, a);
         }
@@ -189,7 +226,7 @@ __global__ __launch_bounds__(NT) void block_norm_bwd_kernel(BlockNormBwdArgs g)
                 for (int j = 0; j < 8; ++j) {
                     const float dy = (float)a.dy[i][j], n = h[j] * a.rstd;
                     sum = fmaf(dy * (HOLD ? hw[HOLD ? i : 0][j] : w[j]), n, sum);
-                    dw[i][j] = fmaf(dy, n, dw[i][j]);
+                    dw(i, j) = fmaf(dy, n, dw(i, j));
                 }
             }
             mean = row_sum<NT, L>(sum, slot[turn]) / (float)g.cols;
@@ -219,7 +256,7 @@ __global__ __launch_bounds__(NT) void block_norm_bwd_kernel(BlockNormBwdArgs g)
                 if (read_o) {
                     const float m = o[j] * a.rstd_post;
                     sum = fmaf(p[i][j], m, sum);
-                    t[i][j] = fmaf(d, m, t[i][j]);
+                    t(i, j) = fmaf(d, m, t(i, j));
                 }
             }
             if (g.DX && col(i) < g.cols)
@@ -250,22 +287,35 @@ __global__ __launch_bounds__(NT) void block_norm_bwd_kernel(BlockNormBwdArgs g)
                                      : g.ws + (2 * (int64_t)g.groups + 2 * walker + (first > r0)) * g.cols;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    float v[8];
+                    float v[8], sum_t[8];
                     weights8<T>(g.G, gr * g.ldg, g.w_f32, col(i), g.cols, v);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        held(i, j) = fmaf(v[j], t[i][j], held(i, j));
+                    for (int j = 0; j < 8; ++j) {
+                        sum_t[j] = t(i, j);
+                        t(i, j) = 0.0f;
+                    }
+                    if constexpr (FAR) {
+                        if (g.DWP && col(i) < g.cols) {
+                            float old[8];
+                            row_load8<false>(place, col(i), g.cols, old);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                old[j] = fmaf(v[j], sum_t[j], old[j]);
+                            row_store8(place, col(i), g.cols, old);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            held(i, j) = fmaf(v[j], sum_t[j], held(i, j));
+                    }
                     if (out && whole) {
                         weights8<T>(g.WP, 0, g.w_f32, col(i), g.cols, v);
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            t[i][j] *= v[j];
+                            sum_t[j] *= v[j];
                     }
                     if (out && col(i) < g.cols)
-                        row_store8(out, col(i), g.cols, t[i]);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        t[i][j] = 0.0f;
+                        row_store8(out, col(i), g.cols, sum_t);
                 }
                 if (row + 1 < r1) {
                     ++gr;
@@ -279,57 +329,66 @@ __global__ __launch_bounds__(NT) void block_norm_bwd_kernel(BlockNormBwdArgs g)
             }
         }
     }
-    // the workgroup's sums: of d m or gate d m, and of dy n
-    if constexpr (SEVERAL) {
+    // the workgroup's sums: of dy n, and of d m or gate d m
+    if constexpr (FAR) {
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+        for (int k = 0; k < 3; ++k) {
+            if (k == 0 ? !g.DW : SEVERAL || (!g.DWP && (k == 2 || !g.DG)) || (k == 2 && g.team == g.groups))
+                continue;
+            float *out = g.ws + ((int64_t)k * g.groups + walk.group) * g.cols;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                t[i][j] = held(i, j);
+            for (int i = 0; i < V; ++i) {
+                float v[8];
+                weights8<T>(k == 2 ? g.G : nullptr, gr * g.ldg, g.w_f32, col(i), g.cols, v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[j] *= k == 0 ? dw(i, j) : t(i, j);
+                if (col(i) < g.cols)
+                    row_store8(out, col(i), g.cols, v);
+            }
+        }
+    } else {
+        if constexpr (SEVERAL) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    rt[FAR ? 0 : i][j] = held(i, j);
+        }
+        if (g.DW)
+            block_norm_put_sums<NT, L, V>(g.ws + (int64_t)walk.group * g.cols, sums, lane, own, g.cols, rdw);
+        if (SEVERAL ? g.DWP != nullptr : g.DWP || g.DG)
+            block_norm_put_sums<NT, L, V>(place, sums, lane, own, g.cols, rt);
+        if (!SEVERAL && g.DWP && g.team < g.groups) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float v[8];
+                weights8<T>(g.G, gr * g.ldg, g.w_f32, col(i), g.cols, v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    rt[FAR ? 0 : i][j] *= v[j];
+            }
+            block_norm_put_sums<NT, L, V>(place + (int64_t)g.groups * g.cols, sums, lane, own, g.cols, rt);
+        }
     }
-    if (g.DW)
-        block_norm_put_sums<NT, L, V>(g.ws + (int64_t)blockIdx.x * g.cols, sums, lane, own, g.cols, dw);
-    if (SEVERAL ? g.DWP != nullptr : g.DWP || g.DG)
-        block_norm_put_sums<NT, L, V>(g.ws + ((int64_t)g.groups + blockIdx.x) * g.cols, sums, lane, own, g.cols, t);
 }
 
-// The same for whole pieces (cols a multiple of 8) with every operand and DX and DO there,
-// one piece a work-item: no conditions in the loop, the next row's values requested as soon
-// as this row's are converted, and n, g, m and p kept from one pass over the row to the next.
-template <typename T, int NT, int L, bool KEPT, bool SEVERAL>
+// The same for whole pieces (cols a multiple of 8) with dy, dh, dx and do, one piece a
+// work-item and one gate a walker: few conditions in the loop, the next row's values requested
+// as soon as this row's are converted, and n, g, m and p kept from one pass over the row to
+// the next.
+template <typename T, int NT, int L, bool KEPT, bool POST>
 __global__ __launch_bounds__(NT) void block_norm_bwd_whole_kernel(BlockNormBwdArgs g)
 {
     typedef typename Elt<T>::Raw Raw;
     typedef Source<T, KEPT> Src;
     constexpr int ROWS = NT / L;
     __shared__ float slot[4][NT / 64];
-    __shared__ float sums[SEVERAL || ROWS > 1 ? NT * 8 : 1];
+    __shared__ float sums[ROWS > 1 ? NT * 8 : 1];
     const int lane = threadIdx.x % L, own = ROWS == 1 ? 0 : threadIdx.x / L;
-    const int64_t walker = (int64_t)blockIdx.x * ROWS + own, r0 = walker * g.chunk;
-    const int64_t r1 = min<int64_t>(g.rows, r0 + g.chunk);
-    const bool live = 8 * lane < g.cols;
+    const BlockNormWalk<false, ROWS> walk(g, own);
+    const bool live = 8 * lane < g.cols, read_o = POST || g.O;
     const int c = live ? 8 * lane : 0;      // (work-items past the row's end take its first piece, and add zeros)
-    auto held = [&](int j) -> float & { return sums[j * NT + threadIdx.x]; };
-
-    int gr = SEVERAL ? (int)((uint32_t)min<int64_t>(r0, g.rows - 1) / (uint32_t)g.gate_rows) : 0;  // the gate's row
-    int64_t gate_end = SEVERAL ? (int64_t)(gr + 1) * g.gate_rows : g.rows;
-    float w[8], gw[8], dw[8], t[8];
-    auto gate_weight = [&] {  // gate * w_post
-        float wp[8];
-        weights8<T>(g.G, gr * g.ldg, g.w_f32, c, g.cols, gw);
-        weights8<T>(g.WP, 0, g.w_f32, c, g.cols, wp);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            gw[j] *= wp[j];
-    };
-    weights8<T>(g.W, 0, g.w_f32, c, g.cols, w);
-    gate_weight();
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        dw[j] = t[j] = 0.0f;
-        if (SEVERAL)
-            held(j) = 0.0f;
-    }
     struct Row {
         Raw dy, dh;
         typename Src::Raw h, o;
@@ -339,31 +398,43 @@ __global__ __launch_bounds__(NT) void block_norm_bwd_whole_kernel(BlockNormBwdAr
         b.dy = Elt<T>::template raw8<true>(static_cast<const T *>(g.DY) + row * g.lddy + c);
         Src::load(b.h, g.H, g.ldh, g.SH, g.ldsh, row, c, c + 8);
         b.dh = Elt<T>::template raw8<true>(static_cast<const T *>(g.DH) + row * g.lddh + c);
-        Src::load(b.o, g.O, g.ldo, g.SO, g.ldso, row, c, c + 8);
+        if (read_o)
+            Src::load(b.o, g.O, g.ldo, g.SO, g.ldso, row, c, c + 8);
         b.rstd = g.rstd[row];
-        b.rstd_post = g.rstd_post[row];
+        b.rstd_post = POST ? g.rstd_post[row] : 1.0f;
     };
-    if (r0 < r1)
-        request(r0);
+    if (walk.first < walk.end)
+        request(walk.first);
+    float w[8], gw[8], wp[8], dw[1][8], t[1][8];
+    weights8<T>(g.W, 0, g.w_f32, c, g.cols, w);
+    weights8<T>(g.G, walk.gate * g.ldg, g.w_f32, c, g.cols, gw);
+    weights8<T>(POST ? g.WP : nullptr, 0, g.w_f32, c, g.cols, wp);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        gw[j] *= wp[j];
+        dw[0][j] = t[0][j] = 0.0f;
+    }
     const float per_col = 1.0f / (float)g.cols;
     int turn = 0;
-    for (int64_t row = r0; row < r1; ++row, turn ^= 1) {
+    for (int64_t row = walk.first; row < walk.end; row += walk.step, turn ^= 1) {
         const float rstd = b.rstd, rp = b.rstd_post;
         float n[8], gy[8], m[8], p[8], dh[8], sum = 0.0f;
         Src::values(b.h, n);
-        Src::values(b.o, m);
+        if (read_o)
+            Src::values(b.o, m);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float dy = (float)b.dy[j];
             n[j] *= rstd;
-            m[j] *= rp;
+            if (POST)
+                m[j] *= rp;
             dh[j] = (float)b.dh[j];
             gy[j] = dy * w[j];
             sum = fmaf(gy[j], n[j], sum);
-            dw[j] = fmaf(dy, n[j], dw[j]);
+            dw[0][j] = fmaf(dy, n[j], dw[0][j]);
         }
-        if (row + 1 < r1)
-            request(row + 1);
+        if (row + walk.step < walk.end)
+            request(row + walk.step);
         const float mean = row_sum<NT, L>(live ? sum : 0.0f, slot[turn]) * per_col;
         float dx[8];
         sum = 0.0f;
@@ -372,57 +443,33 @@ __global__ __launch_bounds__(NT) void block_norm_bwd_whole_kernel(BlockNormBwdAr
             const float d = fmaf(rstd, fmaf(-mean, n[j], gy[j]), dh[j]);
             dx[j] = g.alpha * d;
             p[j] = d * gw[j];
-            sum = fmaf(p[j], m[j], sum);
-            t[j] = fmaf(d, m[j], t[j]);
+            if (POST)
+                sum = fmaf(p[j], m[j], sum);
+            if (read_o)
+                t[0][j] = fmaf(d, m[j], t[0][j]);
         }
         if (live)
             Elt<T>::store8(static_cast<T *>(g.DX) + row * g.lddx + c, dx);
-        const float back = row_sum<NT, L>(live ? sum : 0.0f, slot[2 + turn]) * per_col * rp;
+        if constexpr (POST) {
+            const float back = row_sum<NT, L>(live ? sum : 0.0f, slot[2 + turn]) * per_col * rp;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            p[j] = fmaf(rp, p[j], -back * m[j]);
+            for (int j = 0; j < 8; ++j)
+                p[j] = fmaf(rp, p[j], -back * m[j]);
+        }
         if (live)
             Elt<T>::store8(static_cast<T *>(g.DO) + row * g.lddo + c, p);
-        if constexpr (SEVERAL) {
-            if (row + 1 == r1 || row + 1 == gate_end) {
-                const int64_t first = gate_end - g.gate_rows;
-                const bool whole = first >= r0 && (row + 1 == gate_end || row + 1 == g.rows);
-                float *out = !g.DG ? nullptr
-                             : whole ? g.DG + gr * g.lddg
-                                     : g.ws + (2 * (int64_t)g.groups + 2 * walker + (first > r0)) * g.cols;
-                float v[8];
-                weights8<T>(g.G, gr * g.ldg, g.w_f32, c, g.cols, v);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    held(j) = fmaf(v[j], t[j], held(j));
-                if (out && whole) {
-                    weights8<T>(g.WP, 0, g.w_f32, c, g.cols, v);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        t[j] *= v[j];
-                }
-                if (out && live)
-                    Elt<float>::store8(out + c, t);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    t[j] = 0.0f;
-                if (row + 1 < r1) {
-                    ++gr;
-                    gate_end += g.gate_rows;
-                    gate_weight();
-                }
-            }
-        }
-    }
-    if constexpr (SEVERAL) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            t[j] = held(j);
     }
     if (g.DW)
-        block_norm_put_sums<NT, L, 1>(g.ws + (int64_t)blockIdx.x * g.cols, sums, lane, own, g.cols, &dw);
-    if (SEVERAL ? g.DWP != nullptr : g.DWP || g.DG)
-        block_norm_put_sums<NT, L, 1>(g.ws + ((int64_t)g.groups + blockIdx.x) * g.cols, sums, lane, own, g.cols, &t);
+        block_norm_put_sums<NT, L, 1>(g.ws + (int64_t)walk.group * g.cols, sums, lane, own, g.cols, dw);
+    if (g.DWP || g.DG)
+        block_norm_put_sums<NT, L, 1>(g.ws + ((int64_t)g.groups + walk.group) * g.cols, sums, lane, own, g.cols, t);
+    if (g.DWP && g.team < g.groups) {
+        weights8<T>(g.G, walk.gate * g.ldg, g.w_f32, c, g.cols, gw);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            t[0][j] *= gw[j];
+        block_norm_put_sums<NT, L, 1>(g.ws + (2 * (int64_t)g.groups + walk.group) * g.cols, sums, lane, own, g.cols, t);
+    }
 }
 
 // Work-items of a workgroup and of a row, and pieces per work-item: one piece up to 8192
@@ -443,38 +490,43 @@ void bwd_by_cols(int cols, F f)
     else if (cols <= 4096)
         f.template run<T, 512, 512, 1>();
     else if (cols <= 8192)
-        f.template run<T, 512, 512, 2>();
+        f.template run<T, 1024, 1024, 1>();
     else if (cols <= 16384)
-        f.template run<T, 512, 512, 4>();
+        f.template run<T, 1024, 1024, 2>();
     else
         f.template run<T, 1024, 1024, 4>();
 }
 
-struct Bwd {
+template <bool KEPT> struct Bwd {
     const BlockNormBwdArgs &a;
-    bool kept, several;
     hipStream_t s;
-    template <typename T, int NT, int L, int V, bool KEPT, bool SEVERAL> void go()
+    template <typename T, int NT, int L, int V, bool SEVERAL> void go()
     {
-        if constexpr (V == 1) {
-            if (a.cols % 8 == 0 && a.DY && a.DH && a.DX && a.DO && a.WP) {
-                block_norm_bwd_whole_kernel<T, NT, L, KEPT, SEVERAL><<<(unsigned)a.groups, NT, 0, s>>>(a);
+        if constexpr (V == 1 && !SEVERAL) {
+            if (a.cols % 8 == 0 && a.DY && a.DH && a.DX && a.DO) {
+                if (a.WP)
+                    block_norm_bwd_whole_kernel<T, NT, L, KEPT, true><<<(unsigned)a.groups, NT, 0, s>>>(a);
+                else
+                    block_norm_bwd_whole_kernel<T, NT, L, KEPT, false><<<(unsigned)a.groups, NT, 0, s>>>(a);
                 return;
             }
         }
-        constexpr bool AHEAD = V == 2 && sizeof(T) == 2;
+        constexpr bool AHEAD = V == 1 && NT < 1024;
         block_norm_bwd_kernel<T, NT, L, V, AHEAD, KEPT, SEVERAL><<<(unsigned)a.groups, NT, 0, s>>>(a);
     }
     template <typename T, int NT, int L, int V> void run()
     {
-        kept ? several ? go<T, NT, L, V, true, true>() : go<T, NT, L, V, true, false>()
-             : several ? go<T, NT, L, V, false, true>() : go<T, NT, L, V, false, false>();
+        a.team ? go<T, NT, L, V, false>() : go<T, NT, L, V, true>();
     }
 };
 
 }  // namespace
 
-// The kernels of each type of row are compiled in a file of their own.
-template <typename T> void launch_block_norm_bwd_rows(const BlockNormBwdArgs &a, bool kept, bool several, hipStream_t s);
+// The kernels of each type of row, from kept values or not, are compiled in a file of their own.
+template <typename T, bool KEPT> void launch_block_norm_bwd_from(const BlockNormBwdArgs &a, hipStream_t s);
+template <typename T> void launch_block_norm_bwd_rows(const BlockNormBwdArgs &a, bool kept, hipStream_t s)
+{
+    kept ? launch_block_norm_bwd_from<T, true>(a, s) : launch_block_norm_bwd_from<T, false>(a, s);
+}
 
 }  // namespace sgemm

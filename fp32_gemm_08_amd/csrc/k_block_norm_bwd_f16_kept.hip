@@ -1,0 +1,11 @@
+// Backward pass of the norms around a block for rows of _Float16, h and o kept in 8 bits.
+#include "block_norm_bwd.h"
+
+namespace sgemm {
+
+template <> void launch_block_norm_bwd_from<_Float16, true>(const BlockNormBwdArgs &a, hipStream_t s)
+{
+    bwd_by_cols<_Float16>(a.cols, Bwd<true>{a, s});
+}
+
+}  // namespace sgemm

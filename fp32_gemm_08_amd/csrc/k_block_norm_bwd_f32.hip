@@ -3,9 +3,9 @@
 
 namespace sgemm {
 
-template <> void launch_block_norm_bwd_rows<float>(const BlockNormBwdArgs &a, bool kept, bool several, hipStream_t s)
+template <> void launch_block_norm_bwd_from<float, false>(const BlockNormBwdArgs &a, hipStream_t s)
 {
-    bwd_by_cols<float>(a.cols, Bwd{a, kept, several, s});
+    bwd_by_cols<float>(a.cols, Bwd<false>{a, s});
 }
 
 }  // namespace sgemm

@@ -221,7 +221,7 @@ int sgemm_block_norm_bwd(int type, int w_type, int64_t rows, int64_t cols, const
     a.gate_rows = (int)gate_rows;
     a.alpha = alpha;
     a.w_f32 = w_type == SGEMM_TYPE_F32;
-    a.groups = a.chunk = 0;
+    a.groups = a.team = a.chunk = 0;
     (void)hipGetLastError();
     return finish(launch_block_norm_bwd(a, type, kept == 1, reinterpret_cast<hipStream_t>(stream)));
 }

@@ -30,18 +30,18 @@ struct BlockNormBwdArgs {
     float alpha;
     int w_f32;
     int groups;             // workgroups
-    int chunk;              // consecutive rows of a walker
+    int team;               // of them, those of a gate; 0: several gates a walker
+    int chunk;              // then: consecutive rows of a walker
 };
 
 // Who sums what of the backward pass.  A walker is the work-items that hold a row (a
-// workgroup, or 16 to 64 lanes of one); it takes `chunk` consecutive rows.  With one
-// gate row for all rows a workgroup leaves the sums of dy n and of d m of all its rows.
-// With several it leaves those of dy n and of gate d m, and its walkers leave their sums
-// of d m for those gate rows of which they do not have all rows: for the first that they
-// meet at 2 * walker, for another one (the last) at 2 * walker + 1.
+// workgroup, or 16 to 64 lanes of one).  Few gates: each has a team of workgroups, which
+// leave their sums of dy n, of d m and (more gates than one) of gate d m.  Many: a walker
+// takes `chunk` consecutive rows, its workgroup leaves the sums of dy n and of gate d m, and
+// walkers leave their sums of d m for those gates of which they do not have all rows: for
+// the first that they meet at 2 * walker, for another one (the last) at 2 * walker + 1.
 struct BlockNormSums {
-    int64_t groups = 0, walkers = 0, chunk = 1;
-    bool several = false;
+    int64_t groups = 0, team = 0, walkers = 0, chunk = 1;
     int64_t parts = 0;      // arrays of cols floats in the workspace
 };
 BlockNormSums block_norm_sums(int64_t rows, int64_t cols, int64_t gate_rows);

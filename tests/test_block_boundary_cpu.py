@@ -203,7 +203,7 @@ def test_bwd_quick_returns_and_plan():
                 st, nb = plan(rows, cols, gate_rows)
                 assert st == OK and 0 < nb <= 128 << 20 and nb % (4 * cols) == 0
     assert plan(16384, 4096, 0) == plan(16384, 4096, 16384) == plan(16384, 4096, 1 << 40)
-    assert plan(16384, 4096, 2048)[1] > plan(16384, 4096, 0)[1]
+    assert plan(16384, 4096, 64)[1] > plan(16384, 4096, 2048)[1] > plan(16384, 4096, 0)[1]
     assert plan(0, 300, 5) == (OK, 0)
     assert plan(-1, 300, 0)[0] == INVALID and plan(1, lib.RMSNORM_MAX_COLS + 1, 0)[0] == INVALID and plan(1, 1, -1)[0] == INVALID
 

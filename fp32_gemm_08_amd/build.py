@@ -1,4 +1,5 @@
-"""Build libsgemm_f32.so in-tree with hipcc for gfx950.
+"""Build libsgemm_f32.so in-tree with hipcc for gfx950, and _tensors.so, the Python module
+that calls it with torch tensors, with g++ against torch's headers.
 
     python -m fp32_gemm_08_amd.build
 
@@ -8,10 +9,12 @@ out of the device code (``-packed-fp32-ops``); no fast-math flags are used.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsgemm_f32.so")
+TENSORS = os.path.join(PKG, "_tensors.so")
 
 SOURCES = ["sgemm_api.cpp", "k_naive.hip", "k_tiled.hip", "k_regblock.hip", "k_mfma.hip", "k_mfma_lp.hip", "k_lp16.hip", "k_splitk.hip",
            "k_transpose.hip", "k_probe.hip", "f8_api.cpp", "k_f8_gemm.hip", "k_f8_skinny.hip", "k_f8_large.hip", "k_f8_small.hip",
@@ -49,6 +53,23 @@ def _compile(src: str, extra) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed for {src}:\n{r.stdout}\n{r.stderr}")
     return obj
+
+
+def _build_tensors() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch not found (its headers are required to build _tensors.so)")
+    torch = os.path.dirname(spec.origin)
+    inc = os.path.join(torch, "include")
+    tmp = TENSORS + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE, "-isystem", inc, "-isystem",
+           os.path.join(inc, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "tensors.cpp"), "-o", tmp, "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for tensors.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TENSORS)
+    return TENSORS
 
 
 # Debug variants, built next to the library on request and loaded through
@@ -96,7 +117,10 @@ def build(verbose: bool = False, extra=(), variant: str = "") -> str:
 def _build(verbose, extra, lib, variant) -> str:
     os.makedirs(BUILD, exist_ok=True)
     with ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
+        tensors = None if variant else ex.submit(_build_tensors)
         objs = list(ex.map(lambda s: _compile(s, extra), SOURCES))
+        if tensors:
+            tensors.result()
     link_extra = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
                   "-Xarch_host", "-shared-libsan"] if variant == "sanitize" else []
     tmp = lib + ".tmp"

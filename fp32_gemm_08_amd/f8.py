@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 
+from .native import check, tensors
 from .sgemm import SGEMM_OK, SgemmError, load, sgemm_f32_status_string
 
 F8_FORMAT = {"e4m3": 1, "e5m2": 2}
@@ -279,15 +280,7 @@ def f8_requantize(X, SX, QT, ST, stream=None):
     rows of X: a product over the rows takes it, without the 16-bit values having
     been kept.
     """
-    dev = _device(X)
-    fx, rows, cols, px, ldx = _matrix("X", X, _FORMAT_OF, dev)
-    fq, r, c, pq, ldq = _matrix("QT", QT, _FORMAT_OF, dev)
-    if (r, c) != (cols, rows):
-        raise ValueError(f"QT has shape {(r, c)}, not {(cols, rows)}")
-    psx, ldsx = _scale("SX", SX, (_blocks(cols), rows), dev)
-    pst, ldst = _scale("ST", ST, (_blocks(rows), cols), dev)
-    _run(dev, stream, _load_f8().sgemm_f8_requantize,
-         (fx, fq, rows, cols, px, ldx, psx, ldsx, pq, ldq, pst, ldst))
+    check(tensors().f8_requantize(X, SX, QT, ST, stream))
 
 
 def rmsnorm(X, W, eps=1e-6, residual=None, H=None, Y=None, Q=None, S=None, rstd=None, stream=None):

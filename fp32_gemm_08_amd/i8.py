@@ -10,8 +10,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import f8
-from .f8 import _device, _matrix, _run, _vector, _workspace
+from .native import check, tensors
 from .sgemm import load
 
 I8_MAX_K = 131071
@@ -20,7 +19,6 @@ I8_MAX_K = 131071
 I8_EXPORTS = ("sgemm_i8_gemm", "sgemm_i8_gemm_plan", "sgemm_i8_gemm_workspace", "sgemm_i8_quantize")
 
 _i8 = None
-_I8 = None  # torch dtype of 8-bit integers -> 0
 
 
 def _load_i8():
@@ -70,15 +68,6 @@ def sgemm_i8_quantize(x_type, rows, cols, X, ldx, Q, ldq, S, stream=0) -> int:
 
 # ---------------------------------------------------------------- over torch tensors
 
-def _i8_table():
-    global _I8
-    if _I8 is None:
-        import torch
-
-        _I8 = {torch.int8: 0}
-    return _I8
-
-
 def i8_gemm(A, SA, B, SB, C, alpha=1.0, beta=0.0, workspace=None, stream=None):
     """C <- alpha*diag(SA)*A*B^T*diag(SB) + beta*C, in place; returns C.
 
@@ -90,18 +79,7 @@ def i8_gemm(A, SA, B, SB, C, alpha=1.0, beta=0.0, workspace=None, stream=None):
     boundaries (sgemm_i8_gemm_workspace says how many bytes serve; the call takes
     the fastest way that fits, with the same result).
     """
-    dev = _device(C)
-    i8 = _I8 or _i8_table()
-    _, M, K, pa, lda = _matrix("A", A, i8, dev)
-    _, N, kb, pb, ldb = _matrix("B", B, i8, dev)
-    ct, mc, nc, pc, ldc = _matrix("C", C, f8._TYPE_OF, dev)
-    if kb != K or mc != M or nc != N:
-        raise ValueError(f"shape mismatch: A {(M, K)}, B {(N, kb)}, C {(mc, nc)}")
-    psa = _vector("SA", SA, M, dev, f8._F32)[1]
-    psb = _vector("SB", SB, N, dev, f8._F32)[1]
-    pw, nw = _workspace(workspace, dev)
-    _run(dev, stream, (_i8 or _load_i8()).sgemm_i8_gemm,
-         (ct, M, N, K, alpha, pa, lda, psa, pb, ldb, psb, beta, pc, ldc, pw, nw))
+    check(tensors().i8_gemm(A, SA, B, SB, C, alpha, beta, workspace, stream))
     return C
 
 
@@ -109,10 +87,4 @@ def i8_quantize(X, Q, S, stream=None):
     """X (rows, cols; float32, float16 or bfloat16) -> Q (rows, cols; int8) with one
     scale per row in S (rows, float32): Q is 127 * X / max|X| of the row to the
     nearest integer, ties to even, and Q * S is about X."""
-    dev = _device(X)
-    xt, rows, cols, px, ldx = _matrix("X", X, f8._TYPE_OF, dev)
-    _, r, c, pq, ldq = _matrix("Q", Q, _I8 or _i8_table(), dev)
-    if r != rows or c != cols:
-        raise ValueError(f"Q has shape {(r, c)}, not {(rows, cols)}")
-    ps = _vector("S", S, rows, dev, f8._F32)[1]
-    _run(dev, stream, (_i8 or _load_i8()).sgemm_i8_quantize, (xt, rows, cols, px, ldx, pq, ldq, ps))
+    check(tensors().i8_quantize(X, Q, S, stream))

@@ -27,7 +27,7 @@ TENSORS = os.path.join(PKG, "_tensors.so")
 
 SOURCES = ["sgemm_api.cpp", "k_naive.hip", "k_tiled.hip", "k_regblock.hip", "k_mfma.hip", "k_mfma_lp.hip", "k_lp16.hip", "k_splitk.hip",
            "k_transpose.hip", "k_probe.hip", "f8_api.cpp", "k_f8_gemm.hip", "k_f8_skinny.hip", "k_f8_large.hip", "k_f8_small.hip",
-           "k_f8_quant.hip", "k_norm.hip", "norm_api.cpp", "k_block_norm.hip", "k_block_norm_bwd_f32.hip", "k_block_norm_bwd_f32_kept.hip",
+           "k_f8_quant.hip", "k_f8_requant.hip", "k_norm.hip", "norm_api.cpp", "k_block_norm.hip", "k_block_norm_bwd_f32.hip", "k_block_norm_bwd_f32_kept.hip",
            "k_block_norm_bwd_f16.hip", "k_block_norm_bwd_f16_kept.hip", "k_block_norm_bwd_bf16.hip", "k_block_norm_bwd_bf16_kept.hip", "k_block_norm_sums.hip", "i8_api.cpp", "k_i8_gemm.hip", "k_i8_skinny.hip", "k_i8_tiles.hip",
            "k_i8_quant.hip"]
 ARCH = "gfx950"

@@ -76,7 +76,7 @@ struct F8QuantArgs {
     int64_t ldsx = 0;
 };
 // The transposed output alone, from an X in 8 bits with row blocks.
-hipError_t launch_f8_requantize(F8QuantArgs a, int format_x, int format, hipStream_t s);
+hipError_t launch_f8_requantize(const F8QuantArgs &a, int format_x, int format, hipStream_t s);
 hipError_t launch_f8_quantize(F8QuantArgs a, bool tile, int format, int x_type, hipStream_t s);
 
 struct NormArgs {

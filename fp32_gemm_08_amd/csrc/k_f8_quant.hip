@@ -19,29 +19,6 @@ namespace {
 constexpr int QT = 128;          // tile side
 constexpr int QT_PITCH = QT + 8; // bytes per column in the transposed tile
 
-// A piece's row of X: values of T, or 8-bit ones of a format with the scales of their row
-// blocks (of column tile `tc`).
-template <int FMT> struct F8In {};
-template <typename T> struct Input {
-    static __device__ __forceinline__ void load(const F8QuantArgs &g, int r, int c, int, float (&v)[8])
-    {
-        row_load8<true>(static_cast<const T *>(g.X) + (int64_t)r * g.ldx, c, g.cols, v);
-    }
-};
-template <int FMT> struct Input<F8In<FMT>> {
-    static __device__ __forceinline__ void load(const F8QuantArgs &g, int r, int c, int tc, float (&v)[8])
-    {
-        const f8_u32x2 q = row_raw8b<true>(static_cast<const uint8_t *>(g.X) + (int64_t)r * g.ldx, c, g.cols);
-        const float s = g.SX[(int64_t)tc * g.ldsx + r];
-        f8_unpack8<FMT>(q, v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            v[j] *= s;
-        // (a NaN or infinite scale makes NaN of the zeros past the row's end too: they are in
-        // no other column's block, and in this row's, which is not asked for)
-    }
-};
-
 template <typename T, int FMT, bool TILE>
 __global__ __launch_bounds__(256) void f8_quantize_kernel(F8QuantArgs g)
 {
@@ -62,7 +39,7 @@ __global__ __launch_bounds__(256) void f8_quantize_kernel(F8QuantArgs g)
     for (int i = 0; i < 8; ++i) {
         const int r = r0 + pr + i;
         if (r < g.rows && c < g.cols) {
-            Input<T>::load(g, r, c, tc, v[i]);
+            row_load8<true>(static_cast<const T *>(g.X) + (int64_t)r * g.ldx, c, g.cols, v[i]);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -194,27 +171,7 @@ void launch_t(const F8QuantArgs &a, unsigned grid, bool tile, int format, hipStr
     }
 }
 
-template <int FMT>
-void launch_from(const F8QuantArgs &a, unsigned grid, int format, hipStream_t s)
-{
-    if (format == SGEMM_F8_E4M3)
-        f8_quantize_kernel<F8In<FMT>, 0, false><<<grid, 256, 0, s>>>(a);
-    else
-        f8_quantize_kernel<F8In<FMT>, 1, false><<<grid, 256, 0, s>>>(a);
-}
-
 }  // namespace
-
-hipError_t launch_f8_requantize(F8QuantArgs a, int format_x, int format, hipStream_t s)
-{
-    const int64_t tr = ((int64_t)a.rows + QT - 1) / QT, tc = ((int64_t)a.cols + QT - 1) / QT;
-    a.tiles_c = (int)tc;
-    if (format_x == SGEMM_F8_E4M3)
-        launch_from<0>(a, (unsigned)(tr * tc), format, s);
-    else
-        launch_from<1>(a, (unsigned)(tr * tc), format, s);
-    return hipGetLastError();
-}
 
 hipError_t launch_f8_quantize(F8QuantArgs a, bool tile, int format, int x_type, hipStream_t s)
 {

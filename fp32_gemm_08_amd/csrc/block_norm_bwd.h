@@ -25,6 +25,13 @@ template <typename T> struct Source<T, false> {
     {
         r = row_raw8<true>(static_cast<const T *>(p) + row * ld, c, cols);
     }
+    // (rows of at least 8; fix() before the values are used)
+    static __device__ __forceinline__ void load_any(Raw &r, const void *p, int64_t ld, const float *, int64_t, int64_t row,
+                                                    int c, int cols)
+    {
+        r = row_any8<true>(static_cast<const T *>(p) + row * ld, c, cols);
+    }
+    static __device__ __forceinline__ void fix(Raw &r, int past) { row_fix8<T>(r, past); }
     static __device__ __forceinline__ void values(const Raw &r, float (&v)[8])
     {
 #pragma unroll
@@ -42,6 +49,18 @@ template <typename T> struct Source<T, true> {
     {
         r.q = row_raw8b<true>(static_cast<const uint8_t *>(p) + row * ld, c, cols);
         r.s = c < cols ? S[(int64_t)(c / F8_BLOCK) * lds + row] : 0.0f;
+    }
+    static __device__ __forceinline__ void load_any(Raw &r, const void *p, int64_t ld, const float *S, int64_t lds,
+                                                    int64_t row, int c, int cols)
+    {
+        r.q = row_any8b<true>(static_cast<const uint8_t *>(p) + row * ld, c, cols);
+        r.s = S[(int64_t)(min(c, cols - 1) / F8_BLOCK) * lds + row];
+    }
+    static __device__ __forceinline__ void fix(Raw &r, int past)
+    {
+        row_fix8b(r.q, past);
+        if (past >= 8)
+            r.s = 0.0f;
     }
     static __device__ __forceinline__ void values(const Raw &r, float (&v)[8])
     {
@@ -373,12 +392,14 @@ __global__ __launch_bounds__(NT) void block_norm_bwd_kernel(BlockNormBwdArgs g)
     }
 }
 
-// The same for whole pieces (cols a multiple of 8) with dy, dh, dx and do, one piece a
-// work-item and one gate a walker: few conditions in the loop, the next row's values requested
-// as soon as this row's are converted, and n, g, m and p kept from one pass over the row to
-// the next.
-template <typename T, int NT, int L, bool KEPT, bool POST>
-__global__ __launch_bounds__(NT) void block_norm_bwd_whole_kernel(BlockNormBwdArgs g)
+// The same with dy, dh, dx and do, one piece a work-item and one gate a walker: few
+// conditions in the loop, the next row's values requested as soon as this row's are
+// converted, and n, g, m and p kept from one pass over the row to the next.  TAIL: the row's
+// last piece may be shorter (rows of at least 8); its wavefront alone moves what it loaded
+// (as it does in the other kernel, before the next row is requested, which then waits for
+// memory: 16384 x 4095 330 us).
+template <typename T, int NT, int L, bool KEPT, bool POST, bool TAIL>
+__global__ __launch_bounds__(NT) void block_norm_bwd_all_kernel(BlockNormBwdArgs g)
 {
     typedef typename Elt<T>::Raw Raw;
     typedef Source<T, KEPT> Src;
@@ -388,18 +409,21 @@ __global__ __launch_bounds__(NT) void block_norm_bwd_whole_kernel(BlockNormBwdAr
     const int lane = threadIdx.x % L, own = ROWS == 1 ? 0 : threadIdx.x / L;
     const BlockNormWalk<false, ROWS> walk(g, own);
     const bool live = 8 * lane < g.cols, read_o = POST || g.O;
-    const int c = live ? 8 * lane : 0;      // (work-items past the row's end take its first piece, and add zeros)
+    // work-items past the row's end take its first piece and add zeros, or (TAIL) have zeros
+    const int c = live || TAIL ? 8 * lane : 0, cols = TAIL ? g.cols : c + 8;
+    const int past = c + 8 - cols;
+    const bool moves = TAIL && __ballot(past > 0) != 0;
     struct Row {
         Raw dy, dh;
         typename Src::Raw h, o;
         float rstd, rstd_post;
     } b;
     auto request = [&](int64_t row) {
-        b.dy = Elt<T>::template raw8<true>(static_cast<const T *>(g.DY) + row * g.lddy + c);
-        Src::load(b.h, g.H, g.ldh, g.SH, g.ldsh, row, c, c + 8);
-        b.dh = Elt<T>::template raw8<true>(static_cast<const T *>(g.DH) + row * g.lddh + c);
+        b.dy = row_any8<true>(static_cast<const T *>(g.DY) + row * g.lddy, c, cols);
+        Src::load_any(b.h, g.H, g.ldh, g.SH, g.ldsh, row, c, cols);
+        b.dh = row_any8<true>(static_cast<const T *>(g.DH) + row * g.lddh, c, cols);
         if (read_o)
-            Src::load(b.o, g.O, g.ldo, g.SO, g.ldso, row, c, c + 8);
+            Src::load_any(b.o, g.O, g.ldo, g.SO, g.ldso, row, c, cols);
         b.rstd = g.rstd[row];
         b.rstd_post = POST ? g.rstd_post[row] : 1.0f;
     };
@@ -419,6 +443,13 @@ __global__ __launch_bounds__(NT) void block_norm_bwd_whole_kernel(BlockNormBwdAr
     for (int64_t row = walk.first; row < walk.end; row += walk.step, turn ^= 1) {
         const float rstd = b.rstd, rp = b.rstd_post;
         float n[8], gy[8], m[8], p[8], dh[8], sum = 0.0f;
+        if (moves) {
+            row_fix8<T>(b.dy, past);
+            row_fix8<T>(b.dh, past);
+            Src::fix(b.h, past);
+            if (read_o)
+                Src::fix(b.o, past);
+        }
         Src::values(b.h, n);
         if (read_o)
             Src::values(b.o, m);
@@ -449,7 +480,7 @@ __global__ __launch_bounds__(NT) void block_norm_bwd_whole_kernel(BlockNormBwdAr
                 t[0][j] = fmaf(d, m[j], t[0][j]);
         }
         if (live)
-            Elt<T>::store8(static_cast<T *>(g.DX) + row * g.lddx + c, dx);
+            row_store8(static_cast<T *>(g.DX) + row * g.lddx, c, cols, dx);
         if constexpr (POST) {
             const float back = row_sum<NT, L>(live ? sum : 0.0f, slot[2 + turn]) * per_col * rp;
 #pragma unroll
@@ -457,7 +488,7 @@ __global__ __launch_bounds__(NT) void block_norm_bwd_whole_kernel(BlockNormBwdAr
                 p[j] = fmaf(rp, p[j], -back * m[j]);
         }
         if (live)
-            Elt<T>::store8(static_cast<T *>(g.DO) + row * g.lddo + c, p);
+            row_store8(static_cast<T *>(g.DO) + row * g.lddo, c, cols, p);
     }
     if (g.DW)
         block_norm_put_sums<NT, L, 1>(g.ws + (int64_t)walk.group * g.cols, sums, lane, own, g.cols, dw);
@@ -503,11 +534,17 @@ template <bool KEPT> struct Bwd {
     template <typename T, int NT, int L, int V, bool SEVERAL> void go()
     {
         if constexpr (V == 1 && !SEVERAL) {
-            if (a.cols % 8 == 0 && a.DY && a.DH && a.DX && a.DO) {
-                if (a.WP)
-                    block_norm_bwd_whole_kernel<T, NT, L, KEPT, true><<<(unsigned)a.groups, NT, 0, s>>>(a);
+            if (a.DY && a.DH && a.DX && a.DO && a.cols >= 8) {
+                const dim3 grid((unsigned)a.groups), block(NT);
+                const bool whole = a.cols % 8 == 0;
+                if (a.WP && whole)
+                    block_norm_bwd_all_kernel<T, NT, L, KEPT, true, false><<<grid, block, 0, s>>>(a);
+                else if (a.WP)
+                    block_norm_bwd_all_kernel<T, NT, L, KEPT, true, true><<<grid, block, 0, s>>>(a);
+                else if (whole)
+                    block_norm_bwd_all_kernel<T, NT, L, KEPT, false, false><<<grid, block, 0, s>>>(a);
                 else
-                    block_norm_bwd_whole_kernel<T, NT, L, KEPT, false><<<(unsigned)a.groups, NT, 0, s>>>(a);
+                    block_norm_bwd_all_kernel<T, NT, L, KEPT, false, true><<<grid, block, 0, s>>>(a);
                 return;
             }
         }

@@ -260,6 +260,33 @@ __device__ __forceinline__ f8_u32x2 row_raw8b(const uint8_t *row, int c, int col
     }
     return f8_u32x2{(uint32_t)v, (uint32_t)(v >> 32)};
 }
+// The same in two steps, so that a load that is requested ahead is not waited for: of rows of
+// at least 8 elements the row's last 8 where the piece at c is shorter or past the end, and,
+// when they are used, the elements that are past the piece's start by `past` = c + 8 - cols
+// moved to the front.
+template <bool STREAM, typename T>
+__device__ __forceinline__ typename Elt<T>::Raw row_any8(const T *row, int c, int cols)
+{
+    return Elt<T>::template raw8<STREAM>(row + min(c, cols - 8));
+}
+template <typename T> __device__ __forceinline__ void row_fix8(typename Elt<T>::Raw &r, int past)
+{
+    if (past >= 8)
+        r = typename Elt<T>::Raw{};
+    else if (past > 0)
+        r = Elt<T>::drop(r, past);
+}
+template <bool STREAM> __device__ __forceinline__ f8_u32x2 row_any8b(const uint8_t *row, int c, int cols)
+{
+    return row_raw8b<STREAM>(row + min(c, cols - 8), 0, 8);
+}
+__device__ __forceinline__ void row_fix8b(f8_u32x2 &q, int past)
+{
+    if (past > 0) {
+        const uint64_t v = past >= 8 ? 0 : (q[0] | (uint64_t)q[1] << 32) >> (8 * past);
+        q = f8_u32x2{(uint32_t)v, (uint32_t)(v >> 32)};
+    }
+}
 // What 8 bytes of that format stand for, without their scale.
 template <int FMT>
 __device__ __forceinline__ void f8_unpack8(f8_u32x2 q, float (&v)[8])

@@ -11,13 +11,34 @@
 namespace sgemm {
 namespace {
 
+// Zeros past the row's end, at the cost of a branch in the wavefronts that do not reach it.
+__device__ __forceinline__ void zero_past(float (&v)[8], int c, int cols)
+{
+    if (__ballot(c + 8 > cols)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = c + j < cols ? v[j] : 0.0f;
+    }
+}
+
+// The largest |v| as bits, by the maximum that carries a NaN through, whose operands take an
+// absolute value for nothing.
+__device__ __forceinline__ uint32_t abs_maximum8(const float (&v)[8])
+{
+    float m = fabsf(v[0]);
+#pragma unroll
+    for (int j = 1; j < 8; ++j)
+        m = __builtin_elementwise_maximum(m, fabsf(v[j]));
+    return abs_bits(m);
+}
+
 // 8 values in e4m3 with the scale of their block of 128 columns, which 16 consecutive
 // lanes hold (zero past the row's end).
 __device__ __forceinline__ void put_block8(uint8_t *row, float *scale_row, int64_t lds, int c, int cols,
                                            const float (&v)[8])
 {
     float inv, scale;
-    block_scale<0>(max16(abs_max8(v)), inv, scale);
+    block_scale<0>(max16(abs_maximum8(v)), inv, scale);
     if (c < cols) {
         const uint32_t lo = f8_pack4<0>(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
         const uint32_t hi = f8_pack4<0>(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
@@ -84,7 +105,8 @@ __global__ __launch_bounds__(NT) void block_norm_kernel(BlockNormArgs g)
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                h[i][j] = c + j < g.cols ? fmaf(g.alpha, (float)x[i][j], v[j]) : 0.0f;  // (v may be NaN there)
+                h[i][j] = fmaf(g.alpha, (float)x[i][j], v[j]);
+            zero_past(h[i], c, g.cols);  // (v may be NaN there)
         }
     } else {
 #pragma unroll
@@ -121,11 +143,12 @@ __global__ __launch_bounds__(NT) void block_norm_kernel(BlockNormArgs g)
         load_w8<T>(g.W, g.w_f32, c, g.cols, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            h[i][j] = c + j < g.cols ? h[i][j] * rstd * w[j] : 0.0f;
+            h[i][j] = h[i][j] * rstd * w[j];
+        zero_past(h[i], c, g.cols);
         if (g.Y && c < g.cols)
             row_store8(static_cast<T *>(g.Y) + row * g.ldy, c, g.cols, h[i]);
         if (g.Q && g.q_i8)
-            m = max(m, abs_max8(h[i]));
+            m = max(m, abs_maximum8(h[i]));
         else if (g.Q)
             put_block8(g.Q + row * g.ldq, g.S + row, g.lds, c, g.cols, h[i]);
     }

@@ -48,13 +48,24 @@ __device__ __forceinline__ void put_block8(uint8_t *row, float *scale_row, int64
     }
 }
 
+// The workgroup's place among the rows: runs of 32 rows, whose scales of one block share a
+// line, go to one XCD (workgroups go to the 8 in turn), as far as there are whole rounds.
+template <int ROWS> __device__ __forceinline__ int64_t workgroup_rows()
+{
+    constexpr int RUN = ROWS >= 32 ? 1 : 32 / ROWS;
+    const uint32_t b = blockIdx.x, round = b / (8 * RUN);
+    if ((round + 1) * (8 * RUN) > gridDim.x)
+        return b;
+    return (int64_t)round * (8 * RUN) + b % 8 * RUN + b / 8 % RUN;
+}
+
 template <typename T, int NT, int L, int V>
 __global__ __launch_bounds__(NT) void block_norm_kernel(BlockNormArgs g)
 {
     __shared__ float slot[2][NT / 64];
     __shared__ uint32_t top[NT / 64];
     const int lane = threadIdx.x % L;                                    // of the row's
-    const int64_t row = (int64_t)blockIdx.x * (NT / L) + threadIdx.x / L;
+    const int64_t row = workgroup_rows<NT / L>() * (NT / L) + threadIdx.x / L;
     if (row >= g.rows)
         return;  // whole rows of lanes, and only where no row needs the workgroup
     typedef typename Elt<T>::Raw Raw;

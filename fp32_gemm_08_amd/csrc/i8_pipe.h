@@ -53,6 +53,7 @@ __global__ __launch_bounds__(G::NT) void i8_pipe_kernel(I8GemmArgs g)
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = w / G::WGN, wn = w % G::WGN;
     const F8Stages<G, S, false, false> in(i8_as_f8(g), smem, m0, n0, w, split);
+    const I8Scales<MB, FM, FN> scales(g, m0 + wm * G::WM, n0 + wn * G::WN);
 
     typename Blk::Acc acc[FM][FN];
 #pragma unroll
@@ -136,8 +137,8 @@ __global__ __launch_bounds__(G::NT) void i8_pipe_kernel(I8GemmArgs g)
     int *buf = reinterpret_cast<int *>(smem) + w * P::OUT;
 #pragma unroll
     for (int i = 0; i < FM; ++i)
-        i8_store_rows<MB, FN>(g, buf, m0 + wm * G::WM + MB * i, n0 + wn * G::WN, acc[i],
-                              g.ws ? g.ws + (int64_t)split * g.M * g.N : nullptr);
+        i8_store_rows<MB, FM, FN>(g, buf, m0 + wm * G::WM + MB * i, n0 + wn * G::WN, i, acc[i], scales,
+                                  g.ws ? g.ws + (int64_t)split * g.M * g.N : nullptr);
 }
 
 // The same for tiles of few blocks a wavefront: all fragments of the next stage are read
@@ -161,6 +162,7 @@ __global__ __launch_bounds__(G::NT) void i8_flat_kernel(I8GemmArgs g)
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = w / G::WGN, wn = w % G::WGN;
     const F8Stages<G, S, false, false> in(i8_as_f8(g), smem, m0, n0, w, split);
+    const I8Scales<MB, FM, FN> scales(g, m0 + wm * G::WM, n0 + wn * G::WN);
 
     typename Blk::Acc acc[FM][FN];
 #pragma unroll
@@ -224,8 +226,8 @@ __global__ __launch_bounds__(G::NT) void i8_flat_kernel(I8GemmArgs g)
     int *buf = reinterpret_cast<int *>(smem) + w * P::OUT;
 #pragma unroll
     for (int i = 0; i < FM; ++i)
-        i8_store_rows<MB, FN>(g, buf, m0 + wm * G::WM + MB * i, n0 + wn * G::WN, acc[i],
-                              g.ws ? g.ws + (int64_t)split * g.M * g.N : nullptr);
+        i8_store_rows<MB, FM, FN>(g, buf, m0 + wm * G::WM + MB * i, n0 + wn * G::WN, i, acc[i], scales,
+                                  g.ws ? g.ws + (int64_t)split * g.M * g.N : nullptr);
 }
 
 }  // namespace

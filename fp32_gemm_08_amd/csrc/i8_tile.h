@@ -32,14 +32,12 @@ template <int MB> struct I8Frag {
     f8_i32x4 v[NS];
 };
 
-// Columns n .. n+7 of row m of C <- alpha * (v * SA[m]) * SB[n] + beta * C.
+// Columns n .. n+7 of row m of C <- alpha * (v * sa) * sb + beta * C.
 template <typename T>
-__device__ __forceinline__ void i8_put8(const I8GemmArgs &g, int m, int n, const int *v)
+__device__ __forceinline__ void i8_put8(const I8GemmArgs &g, int m, int n, const int *v, float sa, const float (&sb)[8])
 {
     T *row = static_cast<T *>(g.C) + (int64_t)m * g.ldc;
-    const float sa = g.SA[m];
-    float o[8], sb[8];
-    row_load8<false>(g.SB, n, g.N, sb);
+    float o[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         o[i] = g.alpha * ((float)v[i] * sa * sb[i]);
@@ -52,14 +50,14 @@ __device__ __forceinline__ void i8_put8(const I8GemmArgs &g, int m, int n, const
     }
     row_store8(row, n, g.N, o);
 }
-__device__ __forceinline__ void i8_put8(const I8GemmArgs &g, int m, int n, const int *v)
+__device__ __forceinline__ void i8_put8(const I8GemmArgs &g, int m, int n, const int *v, float sa, const float (&sb)[8])
 {
     if (g.c_type == SGEMM_TYPE_F32)
-        i8_put8<float>(g, m, n, v);
+        i8_put8<float>(g, m, n, v, sa, sb);
     else if (g.c_type == SGEMM_TYPE_BF16)
-        i8_put8<__bf16>(g, m, n, v);
+        i8_put8<__bf16>(g, m, n, v, sa, sb);
     else
-        i8_put8<_Float16>(g, m, n, v);
+        i8_put8<_Float16>(g, m, n, v, sa, sb);
 }
 
 // Sums of 8 columns as they are: partial sums [M][N] of a split.
@@ -72,14 +70,33 @@ __device__ __forceinline__ void i8_put_part(int *row, int n, int cols, const int
     row_store8(reinterpret_cast<float *>(row), n, cols, o);
 }
 
-// A wavefront's MB rows of FN blocks of C through `buf` (MB x (MB FN + 4) words of this
-// wavefront's own), so that the lanes of a row write it together.  `part`: this split's
-// partial sums.
-template <int MB, int FN>
-__device__ __forceinline__ void i8_store_rows(const I8GemmArgs &g, int *buf, int m, int n,
-                                              const typename I8Block<MB>::Acc (&acc)[FN], int *part = nullptr)
+// The scales of what a lane writes of its wavefront's FM x FN blocks from (m, n) on, requested
+// before the products: at their end the latency of a first access would be the kernel's.
+template <int MB, int FM, int FN> struct I8Scales {
+    static constexpr int LANES = MB * FN / 8, TURNS = MB * LANES / 64;  // lanes of a row; rows of a lane in a block
+    static_assert(64 % LANES == 0 && TURNS * 64 == MB * LANES, "whole turns of the lanes");
+    float sa[FM][TURNS], sb[8];
+    __device__ __forceinline__ I8Scales(const I8GemmArgs &g, int m, int n)
+    {
+        const int lane = threadIdx.x & 63;
+        row_load8<false>(g.SB, n + 8 * (lane % LANES), g.N, sb);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int t = 0; t < TURNS; ++t)
+                sa[i][t] = g.SA[min(m + MB * i + lane / LANES + t * (64 / LANES), g.M - 1)];
+    }
+};
+
+// A wavefront's MB rows of FN blocks of C, block row i, through `buf` (MB x (MB FN + 4) words
+// of this wavefront's own), so that the lanes of a row write it together.  `part`: this
+// split's partial sums.
+template <int MB, int FM, int FN>
+__device__ __forceinline__ void i8_store_rows(const I8GemmArgs &g, int *buf, int m, int n, int i,
+                                              const typename I8Block<MB>::Acc (&acc)[FN], const I8Scales<MB, FM, FN> &sc,
+                                              int *part = nullptr)
 {
-    constexpr int PITCH = MB * FN + 4, LANES = MB * FN / 8;  // lanes of a row
+    constexpr int PITCH = MB * FN + 4, LANES = MB * FN / 8;
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int j = 0; j < FN; ++j)
@@ -87,16 +104,16 @@ __device__ __forceinline__ void i8_store_rows(const I8GemmArgs &g, int *buf, int
         for (int x = 0; x < MB * MB / 256; ++x)
             *reinterpret_cast<f8_i32x4 *>(buf + lane % MB * PITCH + MB * j + 4 * (lane / MB) + 256 / MB * x) =
                 f8_i32x4{acc[j][4 * x], acc[j][4 * x + 1], acc[j][4 * x + 2], acc[j][4 * x + 3]};
-#pragma unroll 1
-    for (int e = lane; e < MB * LANES; e += 64) {
-        const int r = e / LANES, c = 8 * (e % LANES);
+#pragma unroll
+    for (int t = 0; t < I8Scales<MB, FM, FN>::TURNS; ++t) {
+        const int r = lane / LANES + t * (64 / LANES), c = 8 * (lane % LANES);
         if (m + r >= g.M || n + c >= g.N)
             continue;
         const int *v = buf + r * PITCH + c;
         if (part)
             i8_put_part(part + (int64_t)(m + r) * g.N, n + c, g.N, v);
         else
-            i8_put8(g, m + r, n + c, v);
+            i8_put8(g, m + r, n + c, v, sc.sa[i][t], sc.sb);
     }
 }
 

@@ -21,6 +21,7 @@ __global__ __launch_bounds__(G::NT) void i8_tile_kernel(I8GemmArgs g)
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = w / G::WGN, wn = w % G::WGN;
 
+    const I8Scales<16, G::FM, G::FN> scales(g, m0 + wm * G::WM, n0 + wn * G::WN);
     f8_i32x4 acc[G::FM][G::FN];
 #pragma unroll
     for (int i = 0; i < G::FM; ++i)
@@ -86,7 +87,7 @@ __global__ __launch_bounds__(G::NT) void i8_tile_kernel(I8GemmArgs g)
     int *buf = reinterpret_cast<int *>(smem) + w * G::OUT;
 #pragma unroll
     for (int i = 0; i < G::FM; ++i)
-        i8_store_rows<16, G::FN>(g, buf, m0 + wm * G::WM + 16 * i, n0 + wn * G::WN, acc[i]);
+        i8_store_rows<16, G::FM, G::FN>(g, buf, m0 + wm * G::WM + 16 * i, n0 + wn * G::WN, i, acc[i], scales);
 }
 
 // C from the splits' partial sums, which are integers: their order does not matter.
@@ -95,6 +96,9 @@ __global__ __launch_bounds__(256) void i8_join_kernel(I8GemmArgs g, int splits)
     const int64_t per_row = ((int64_t)g.N + 7) / 8, total = per_row * g.M;
     for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
         const int m = (int)(e / per_row), n = 8 * (int)(e % per_row);
+        const float sa = g.SA[m];
+        float sb[8];
+        row_load8<false>(g.SB, n, g.N, sb);
         int v[8] = {};
         for (int x = 0; x < splits; ++x) {
             float u[8];  // (the bits of integers)
@@ -103,7 +107,7 @@ __global__ __launch_bounds__(256) void i8_join_kernel(I8GemmArgs g, int splits)
             for (int i = 0; i < 8; ++i)
                 v[i] += __float_as_int(u[i]);
         }
-        i8_put8(g, m, n, v);
+        i8_put8(g, m, n, v, sa, sb);
     }
 }
 

@@ -7,14 +7,12 @@ namespace {
 
 // Columns n .. n+3 of row m of C.
 template <typename T>
-__device__ __forceinline__ void i8_put4(const I8GemmArgs &g, int m, int n, f8_i32x4 v)
+__device__ __forceinline__ void i8_put4(const I8GemmArgs &g, int m, int n, f8_i32x4 v, float sa, f8_f32x4 sb)
 {
     typedef T V4 __attribute__((ext_vector_type(4)));
     typedef V4 V4any __attribute__((aligned(1)));
     T *p = static_cast<T *>(g.C) + (int64_t)m * g.ldc + n;
-    const float sa = g.SA[m];
     if (n + 4 <= g.N) {
-        const f8_f32x4 sb = *reinterpret_cast<const f8_f32x4_any *>(g.SB + n);
         f8_f32x4 o;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -34,7 +32,7 @@ __device__ __forceinline__ void i8_put4(const I8GemmArgs &g, int m, int n, f8_i3
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (n + i < g.N) {
-                const float o = g.alpha * ((float)v[i] * sa * g.SB[n + i]);
+                const float o = g.alpha * ((float)v[i] * sa * sb[i]);
                 p[i] = (T)(g.beta != 0.0f ? fmaf(g.beta, (float)p[i], o) : o);
             }
     }
@@ -84,6 +82,14 @@ __global__ __launch_bounds__(512) void i8_skinny_kernel(I8GemmArgs g)
         }
     };
 
+    // the scales of what this lane writes, requested before the products (see I8Scales)
+    static_assert(FM * FN <= NW, "a block per wavefront at the end");
+    const int m = 16 * (w / FN) + l16, n = n0 + 16 * (w % FN) + 4 * q;
+    const float sa = g.SA[min(m, g.M - 1)];
+    f8_f32x4 sb;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        sb[i] = g.SB[min(n + i, g.N - 1)];
     f8_i32x4 acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
@@ -119,31 +125,27 @@ __global__ __launch_bounds__(512) void i8_skinny_kernel(I8GemmArgs g)
             part[w][i * FN + j][lane] = acc[i][j];
     __syncthreads();
     const int used = min(NW, nk);
+    if (w >= FM * FN || m >= g.M || n >= g.N)
+        return;
+    f8_i32x4 v = part[0][w][lane];
+    for (int x = 1; x < used; ++x)
+        v += part[x][w][lane];
+    if (g.ws) {
+        int *p = g.ws + ((int64_t)split * g.M + m) * g.N + n;
+        if (n + 4 <= g.N) {
+            *reinterpret_cast<f8_i32x4_any *>(p) = v;
+        } else {
 #pragma unroll
-    for (int f = w; f < FM * FN; f += NW) {
-        const int m = 16 * (f / FN) + l16, n = n0 + 16 * (f % FN) + 4 * q;
-        if (m >= g.M || n >= g.N)
-            continue;
-        f8_i32x4 v = part[0][f][lane];
-        for (int x = 1; x < used; ++x)
-            v += part[x][f][lane];
-        if (g.ws) {
-            int *p = g.ws + ((int64_t)split * g.M + m) * g.N + n;
-            if (n + 4 <= g.N) {
-                *reinterpret_cast<f8_i32x4_any *>(p) = v;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    if (n + i < g.N)
-                        p[i] = v[i];
-            }
-        } else if (g.c_type == SGEMM_TYPE_F32)
-            i8_put4<float>(g, m, n, v);
-        else if (g.c_type == SGEMM_TYPE_BF16)
-            i8_put4<__bf16>(g, m, n, v);
-        else
-            i8_put4<_Float16>(g, m, n, v);
-    }
+            for (int i = 0; i < 3; ++i)
+                if (n + i < g.N)
+                    p[i] = v[i];
+        }
+    } else if (g.c_type == SGEMM_TYPE_F32)
+        i8_put4<float>(g, m, n, v, sa, sb);
+    else if (g.c_type == SGEMM_TYPE_BF16)
+        i8_put4<__bf16>(g, m, n, v, sa, sb);
+    else
+        i8_put4<_Float16>(g, m, n, v, sa, sb);
 }
 
 }  // namespace

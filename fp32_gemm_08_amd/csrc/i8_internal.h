@@ -8,7 +8,7 @@ namespace sgemm {
 
 enum I8KernelId : int {
     KID_I8_NONE = 0,
-    KID_I8_SKINNY = 90,   // up to 16 rows of A: 16 or 32 columns of C per workgroup, k split over its wavefronts
+    KID_I8_SKINNY = 90,   // up to 16 rows of A (32 where B is small): 16 or 32 columns of C per workgroup, k split over its wavefronts
     KID_I8_ANY = 91,      // rows at any alignment: 64 x 64 tile
     KID_I8_S = 92,        // 64 x 64 tile, two workgroups to a CU
     KID_I8_N = 93,        // 128 x 64 tile
@@ -40,7 +40,7 @@ struct I8GemmPlan {
 // operands where they are; may_pack: operands may be laid out anew in the workspace.
 I8GemmPlan i8_gemm_plan(int64_t M, int64_t N, int64_t K, bool aligned, int64_t room, bool may_pack);
 hipError_t launch_i8_gemm(I8GemmArgs a, const I8GemmPlan &p, hipStream_t s);
-// Up to 16 rows of A, with 16 or 32 columns a workgroup.
+// Up to 32 rows of A, with 16 columns a workgroup, or 32 columns for up to 16 rows.
 hipError_t launch_i8_skinny(const I8GemmArgs &a, int cols, int splits, hipStream_t s);
 // The pipelined kernel of a tile (KID_I8_S to KID_I8_L).
 hipError_t launch_i8_tile(const I8GemmArgs &a, int kid, int splits, hipStream_t s);

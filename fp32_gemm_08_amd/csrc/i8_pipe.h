@@ -37,6 +37,11 @@ struct I8Geo {
 // every wavefront has read all of this stage: there the wavefronts meet, the stage S ahead
 // is requested into its place, and the next stage's fragments are read under the last row's
 // products.
+//
+// Bound by the matrix cores at the clock that power leaves them: 8192^3 to bf16 419 us,
+// 2.62 Pop/s, from 944 with a tile that goes through registers into the LDS; the cores are
+// busy 57 to 61% of the cycles at 1.76 to 1.97 GHz.  Operands of zeros take 405 us, operands
+// that stay in the L2 336 to 357.
 template <class G, int S, int MB>
 __global__ __launch_bounds__(G::NT) void i8_pipe_kernel(I8GemmArgs g)
 {
@@ -144,7 +149,8 @@ __global__ __launch_bounds__(G::NT) void i8_pipe_kernel(I8GemmArgs g)
 // The same for tiles of few blocks a wavefront: all fragments of the next stage are read
 // before this stage's products, into a second set of registers.  The wavefronts meet once a
 // step, when each has its set: the stage S ahead is requested into the place of the one in
-// the registers.
+// the registers.  64 x 16384 x 4096 from memory 17.9 us (3.9 TB/s of B's bytes; 13.2 with B
+// still in the cache behind the L2), 23.7 on the tile that goes through registers.
 template <class G, int S, int MB>
 __global__ __launch_bounds__(G::NT) void i8_flat_kernel(I8GemmArgs g)
 {

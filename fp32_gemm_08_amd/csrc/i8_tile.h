@@ -11,20 +11,12 @@ namespace sgemm {
 // of 4 consecutive ones, the first at 4 * (l / MB), each next one 256 / MB further.  Lane l
 // supplies of row l % MB of each operand 16 consecutive values for a slice of 1024 / MB
 // values of k, at chunk l / MB of the slice (which place is free as long as both agree).
-typedef int i8_i32x16 __attribute__((ext_vector_type(16)));
 template <int MB> struct I8Block;
 template <> struct I8Block<16> {
     typedef f8_i32x4 Acc;
     static __device__ __forceinline__ Acc mma(f8_i32x4 b, f8_i32x4 a, Acc c)
     {
         return __builtin_amdgcn_mfma_i32_16x16x64_i8(b, a, c, 0, 0, 0);
-    }
-};
-template <> struct I8Block<32> {
-    typedef i8_i32x16 Acc;
-    static __device__ __forceinline__ Acc mma(f8_i32x4 b, f8_i32x4 a, Acc c)
-    {
-        return __builtin_amdgcn_mfma_i32_32x32x32_i8(b, a, c, 0, 0, 0);
     }
 };
 template <int MB> struct I8Frag {

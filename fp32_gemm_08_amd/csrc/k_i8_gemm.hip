@@ -157,6 +157,12 @@ I8GemmPlan plan_tiles(int64_t M, int64_t N, int64_t K, int64_t room, double &us)
 // Up to 16 rows: 16 columns per workgroup, 32 where that still leaves two workgroups to
 // each CU (16 x 16384 x 4096 20.0 / 15.7 us, 8 x 8192 x 8192 16.2 / 19.4), k split where
 // few workgroups go through a long k (1 x 1024 x 16384 11.9 us, in 8 parts 6.8 and the join).
+// Up to 32 rows the same with two blocks of rows, as long as one workgroup to a CU covers the
+// columns and A's rows, which every workgroup reads, are short (64 x 64 tiles / this: 32 x 4096
+// x 4096 10.8 / 8.5 us, 32 x 1024 x 8192 14.9 / 11.6, 17 x 500 x 1000 packed 8.6 / 4.2; but 32 x
+// 8192 x 4096 13.6 / 14.9, 32 x 4096 x 16384 21.6 / 24.7).  With four blocks 64 x 4096 x 4096
+// took 12.1 against the tiles' 12.4, 64 x 8192 x 4096 22.6 against 14.6.
+bool skinny(int64_t M, int64_t N, int64_t K) { return M <= 16 || (M <= 32 && N <= 4096 && K <= 8192); }
 int skinny_cols(int64_t N) { return N < 16384 ? 16 : 32; }
 
 I8GemmPlan plan_skinny(int64_t M, int64_t N, int64_t K, int64_t room)
@@ -184,7 +190,7 @@ I8GemmPlan plan_skinny(int64_t M, int64_t N, int64_t K, int64_t room)
 // takes longer, are first laid out anew in the workspace with rows of whole lines.
 I8GemmPlan i8_gemm_plan(int64_t M, int64_t N, int64_t K, bool aligned, int64_t room, bool may_pack)
 {
-    if (M <= 16)
+    if (skinny(M, N, K))
         return plan_skinny(M, N, K, room);
     double us = 0.0;
     if (aligned && N > 1)  // (a single row of B has no distance to the next)

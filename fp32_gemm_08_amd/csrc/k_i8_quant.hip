@@ -6,6 +6,9 @@
 // x * fl(127 / a): two roundings, off by at most 127 * 2^-23 = 1.6e-5.  Only where that
 // lies within 2e-5 of the middle between two integers can it decide wrongly; there
 // 254 x and (2 i + 1) a, which are exact in 64 bits (31 and 32 bits), are compared.
+//
+// Bound by memory: 16384 x 4096 bf16 33.9 us, 5.9 TB/s; packed rows of 4095 40.8, whose
+// stores of 8 bytes straddle lines.  One row of 4096 3.7 us, the launch.
 #include "i8_internal.h"
 #include "norm_rows.h"
 

@@ -41,6 +41,9 @@ __device__ __forceinline__ void i8_put4(const I8GemmArgs &g, int m, int n, f8_i3
 // Up to 16 FM rows of A: a workgroup has 16 FN columns of C, and its 8 wavefronts take the
 // k-blocks of its split in turn, each lane loading its operands straight into registers,
 // DEPTH k-blocks ahead.  The wavefronts' sums are added through the LDS.
+//
+// 1 x 4096 x 4096 5.3 us for 3.3 of B's bytes: a trip to memory, the join and the launch;
+// 16 x 16384 x 4096 15.7, 4.3 TB/s.
 template <int FM, int FN, int DEPTH>
 __global__ __launch_bounds__(512) void i8_skinny_kernel(I8GemmArgs g)
 {
@@ -153,7 +156,9 @@ __global__ __launch_bounds__(512) void i8_skinny_kernel(I8GemmArgs g)
 hipError_t launch_i8_skinny(const I8GemmArgs &a, int cols, int splits, hipStream_t s)
 {
     const unsigned grid = (unsigned)(a.tiles_n * splits);
-    if (cols == 16)
+    if (a.M > 16)
+        i8_skinny_kernel<2, 1, 4><<<grid, 512, 0, s>>>(a);
+    else if (cols == 16)
         i8_skinny_kernel<1, 1, 4><<<grid, 512, 0, s>>>(a);
     else
         i8_skinny_kernel<1, 2, 4><<<grid, 512, 0, s>>>(a);

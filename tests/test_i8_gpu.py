@@ -106,7 +106,8 @@ def test_gemm_larger_and_the_same_with_any_workspace(M, N, K):
 
 # (M, N, K, kernel, splits or 1): every kernel with k that ends within 16 bytes, within a k-block and
 # on its end, one and two k-blocks, splits of unequal length, and edges in both directions
-KERNELS = [(16, 1000, 16384, 90, 4), (3, 500, 12345, 90, 8), (9, 17000, 200, 90, 1), (200, 200, 3000, 92, 4),
+KERNELS = [(16, 1000, 16384, 90, 4), (3, 500, 12345, 90, 8), (9, 17000, 200, 90, 1), (31, 1000, 300, 90, 1),
+           (32, 600, 8192, 90, 8), (25, 4090, 1111, 90, 1), (32, 4100, 200, 92, 1), (200, 200, 3000, 92, 4),
            (33, 1000, 8205, 92, 8), (700, 700, 128, 92, 1), (1000, 999, 129, 92, 1), (510, 4000, 4097, 93, 1),
            (500, 4090, 4080, 93, 1), (1000, 4000, 2049, 94, 1), (1010, 4090, 1920, 94, 1), (2047, 8100, 1000, 95, 1),
            (2040, 8190, 1040, 95, 1), (8100, 8000, 144, 95, 1)]

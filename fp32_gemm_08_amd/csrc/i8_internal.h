@@ -9,7 +9,7 @@ namespace sgemm {
 enum I8KernelId : int {
     KID_I8_NONE = 0,
     KID_I8_SKINNY = 90,   // up to 16 rows of A (32 where B is small): 16 or 32 columns of C per workgroup, k split over its wavefronts
-    KID_I8_ANY = 91,      // rows at any alignment: 64 x 64 tile
+    KID_I8_ANY = 91,      // rows at any alignment: 64 x 64 tile, 4 or 16 wavefronts
     KID_I8_S = 92,        // 64 x 64 tile, two workgroups to a CU
     KID_I8_N = 93,        // 128 x 64 tile
     KID_I8_M = 94,        // 128 x 128 tile

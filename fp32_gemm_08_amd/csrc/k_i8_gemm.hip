@@ -9,17 +9,25 @@ namespace sgemm {
 namespace {
 
 // Rows at any byte address: a k-block of 128 goes through registers into the LDS, the
-// next one is requested before it is multiplied.
-template <class G>
-__global__ __launch_bounds__(G::NT) void i8_tile_kernel(I8GemmArgs g)
+// next one is requested before it is multiplied.  GROUPS times G::NW wavefronts take the
+// k-blocks in turn, each group in a stage of its own; their sums meet in the LDS.
+//
+// 1000 x 1017 x 999 packed 9.2 us, 8 k-blocks: about 10 bytes per CU and cycle however they
+// are loaded (requested 2 or 4 blocks ahead 10.4 to 11.1, two blocks a step 10.4, in words of
+// 4 bytes 15.2): a row's 128 bytes lie in two lines, which the next block needs again.
+template <class G, int GROUPS>
+__global__ __launch_bounds__(G::NT *GROUPS) void i8_tile_kernel(I8GemmArgs g)
 {
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[G::STAGE];
+    constexpr int SUMS = G::BM * G::BN * 4;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[GROUPS * G::STAGE];
     int tm, tn;
     f8_map_tile(blockIdx.x, g.tiles_m, g.tiles_n, tm, tn);
     const int m0 = tm * G::BM, n0 = tn * G::BN;
-    const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4, own = threadIdx.x % G::NT;
+    const int w = __builtin_amdgcn_readfirstlane(own >> 6);
+    const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / G::NT);
     const int wm = w / G::WGN, wn = w % G::WGN;
+    uint8_t *const st = smem + group * G::STAGE;
 
     const I8Scales<16, G::FM, G::FN> scales(g, m0 + wm * G::WM, n0 + wn * G::WN);
     f8_i32x4 acc[G::FM][G::FN];
@@ -33,14 +41,15 @@ __global__ __launch_bounds__(G::NT) void i8_tile_kernel(I8GemmArgs g)
     // past the matrix repeat its last one (their results are not stored)
     constexpr int NC = G::ROWS * 8 / G::NT;
     static_assert(NC * G::NT == G::ROWS * 8 && G::NT % 8 == 0, "whole chunks");
-    const int c = threadIdx.x & 7;
+    const int c = own & 7;
     const uint8_t *row[NC];
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-        const int r = (threadIdx.x + i * G::NT) >> 3;
+        const int r = (own + i * G::NT) >> 3;
         row[i] = (r < G::BM ? g.A + (int64_t)min(m0 + r, g.M - 1) * g.lda
                             : g.B + (int64_t)min(n0 + r - G::BM, g.N - 1) * g.ldb) + 16 * c;
     }
+    const int nkb = (g.K + 127) / 128;
     f8_i32x4 x[NC];
     auto request = [&](int kb) {
         const int valid = min(g.K - kb * 128 - 16 * c, 16);
@@ -53,38 +62,62 @@ __global__ __launch_bounds__(G::NT) void i8_tile_kernel(I8GemmArgs g)
                 x[i] = load16_any(p, valid);
         }
     };
-    const int nkb = (g.K + 127) / 128;
-    request(0);
-    for (int kb = 0; kb < nkb; ++kb) {
-        poison_lds(smem, G::STAGE);
+    if (group < nkb)
+        request(group);
+    // (all groups take as many steps, for the barriers' sake)
+    for (int kb = group; kb - group < nkb; kb += GROUPS) {
+        poison_lds(smem, GROUPS * G::STAGE);
+        if (kb < nkb) {
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int r = (threadIdx.x + i * G::NT) >> 3;
-            *reinterpret_cast<f8_i32x4 *>(smem + r * 128 + 16 * (c ^ f8_swz(r))) = x[i];
+            for (int i = 0; i < NC; ++i) {
+                const int r = (own + i * G::NT) >> 3;
+                *reinterpret_cast<f8_i32x4 *>(st + r * 128 + 16 * (c ^ f8_swz(r))) = x[i];
+            }
         }
         __syncthreads();
-        if (kb + 1 < nkb)
-            request(kb + 1);
+        if (kb + GROUPS < nkb)
+            request(kb + GROUPS);
         auto read = [&](int r, int chunk) {
-            return *reinterpret_cast<const f8_i32x4 *>(smem + r * 128 + 16 * (chunk ^ f8_swz(r)));
+            return *reinterpret_cast<const f8_i32x4 *>(st + r * 128 + 16 * (chunk ^ f8_swz(r)));
         };
+        if (kb < nkb) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            f8_i32x4 b[G::FN];
-#pragma unroll
-            for (int j = 0; j < G::FN; ++j)
-                b[j] = read(G::BM + wn * G::WN + 16 * j + l16, q + 4 * half);
-#pragma unroll
-            for (int i = 0; i < G::FM; ++i) {
-                const f8_i32x4 a = read(wm * G::WM + 16 * i + l16, q + 4 * half);
+            for (int half = 0; half < 2; ++half) {
+                f8_i32x4 b[G::FN];
 #pragma unroll
                 for (int j = 0; j < G::FN; ++j)
-                    acc[i][j] = I8Block<16>::mma(b[j], a, acc[i][j]);
+                    b[j] = read(G::BM + wn * G::WN + 16 * j + l16, q + 4 * half);
+#pragma unroll
+                for (int i = 0; i < G::FM; ++i) {
+                    const f8_i32x4 a = read(wm * G::WM + 16 * i + l16, q + 4 * half);
+#pragma unroll
+                    for (int j = 0; j < G::FN; ++j)
+                        acc[i][j] = I8Block<16>::mma(b[j], a, acc[i][j]);
+                }
             }
         }
         __syncthreads();
     }
-    int *buf = reinterpret_cast<int *>(smem) + w * G::OUT;
+    // the sums of the other groups go to the first, which stores them
+    constexpr int NB = G::FM * G::FN;
+    f8_i32x4 *const sums = reinterpret_cast<f8_i32x4 *>(smem);
+    if (group > 0) {
+#pragma unroll
+        for (int f = 0; f < NB; ++f)
+            sums[((group - 1) * NB + f) * G::NT + own] = acc[f / G::FN][f % G::FN];
+    }
+    if (GROUPS > 1)
+        __syncthreads();
+    if (group > 0)
+        return;
+#pragma unroll
+    for (int x = 0; x < GROUPS - 1; ++x)
+#pragma unroll
+        for (int f = 0; f < NB; ++f)
+            acc[f / G::FN][f % G::FN] += sums[(x * NB + f) * G::NT + own];
+    // (each wavefront passes its rows through a place of its own, behind what others still read)
+    int *buf = reinterpret_cast<int *>(smem + (GROUPS - 1) * SUMS) + w * G::OUT;
+    static_assert((GROUPS - 1) * SUMS + G::NW * G::OUT * 4 <= GROUPS * G::STAGE, "LDS size");
 #pragma unroll
     for (int i = 0; i < G::FM; ++i)
         i8_store_rows<16, G::FM, G::FN>(g, buf, m0 + wm * G::WM + 16 * i, n0 + wn * G::WN, i, acc[i], scales);
@@ -112,6 +145,11 @@ __global__ __launch_bounds__(256) void i8_join_kernel(I8GemmArgs g, int splits)
 }
 
 typedef F8Geo<64, 64, 2, 2> GS;
+// Groups of wavefronts to a workgroup for rows at any alignment: with no more than one tile to
+// a CU, four (1 / 4: 1000 x 1017 x 999 11.6 / 10.2 us, 20 x 8001 x 4001 39.5 / 28.2, 100 x 4001 x
+// 4001 38.1 / 26.6, 300 x 2000 x 5001 22.4 / 23.1); with more, other tiles' workgroups fill the
+// CU (1000 x 2001 x 1001 12.3 / 16.4, 2047^3 36.2 / 51.7).  Two were between them throughout.
+int any_groups(int64_t tiles) { return tiles <= 256 ? 4 : 1; }
 constexpr int64_t kMaxJoin = int64_t{64} << 20;  // bytes of partial sums a call may ask for
 
 // What joining the splits' sums takes, in us.
@@ -199,7 +237,7 @@ I8GemmPlan i8_gemm_plan(int64_t M, int64_t N, int64_t K, bool aligned, int64_t r
     p.kid = KID_I8_ANY;
     p.tiles_m = ceil_div(M, GS::BM);
     p.tiles_n = ceil_div(N, GS::BN);
-    p.threads = GS::NT;
+    p.threads = GS::NT * any_groups(p.tiles_m * p.tiles_n);
     const int64_t ld = f8_packed_ld(K);
     if (may_pack && N > 1 && M <= F8_MAX_PACKED / ld && N <= F8_MAX_PACKED / ld && (M + N) * ld <= room) {
         const int64_t pack = (M + N) * ld;
@@ -247,7 +285,10 @@ hipError_t launch_i8_gemm(I8GemmArgs a, const I8GemmPlan &p, hipStream_t s)
     if (p.kid == KID_I8_SKINNY) {
         e = launch_i8_skinny(a, skinny_cols(a.N), splits, s);
     } else if (p.kid == KID_I8_ANY) {
-        i8_tile_kernel<GS><<<(unsigned)(p.tiles_m * p.tiles_n), GS::NT, 0, s>>>(a);
+        if (any_groups(p.tiles_m * p.tiles_n) == 4)
+            i8_tile_kernel<GS, 4><<<(unsigned)(p.tiles_m * p.tiles_n), p.threads, 0, s>>>(a);
+        else
+            i8_tile_kernel<GS, 1><<<(unsigned)(p.tiles_m * p.tiles_n), p.threads, 0, s>>>(a);
         e = hipGetLastError();
     } else {
         e = launch_i8_tile(a, p.kid, splits, s);

@@ -86,6 +86,13 @@ def test_gemm_any_alignment(M, N, K, offset):
     run_gemm(M, N, K, pad=0, offset=offset, ct="f32")
 
 
+@pytest.mark.parametrize("M,N,K", [(1100, 1090, 300), (1030, 1030, 129), (2100, 600, 1), (1024, 1024, 512), (1020, 1000, 511),
+                                   (70, 4000, 640), (33, 900, 100)])
+def test_gemm_any_alignment_without_a_workspace(M, N, K):
+    assert (-(-M // 64) * -(-N // 64) > 256) == ((M, N) in ((1100, 1090), (1030, 1030), (2100, 600)))   # both of its forms
+    run_gemm(M, N, K, pad=1, offset=1, ws=0)
+
+
 @pytest.mark.parametrize("ct", ["f32", "bf16", "fp16"])
 @pytest.mark.parametrize("M,N,K", [(1, 70, 200), (5, 70, 200), (40, 100, 300), (150, 200, 272), (300, 300, 400)])
 def test_gemm_types(ct, M, N, K):

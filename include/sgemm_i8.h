@@ -40,7 +40,8 @@ extern "C" {
  * where too few output tiles exist to fill the GPU, k is split over workgroups whose
  * partial sums go there; operands at other alignments are laid out there where that
  * is faster.  sgemm_i8_gemm_workspace says how many bytes serve; with fewer, or none,
- * the call takes the fastest way that fits.
+ * the call takes the fastest way that fits.  Calls, and captured graphs, that share a
+ * workspace must not run at once.
  *
  * SGEMM_ERR_INVALID_VALUE: an unknown type; a dimension below 0, K above
  * SGEMM_I8_MAX_K, M or N above 2^31 - 1025; a leading dimension below its row

@@ -75,7 +75,7 @@ int sgemm_block_norm(int type, int w_type, int64_t rows, int64_t cols, const voi
  * DW, DW_post (cols FP32 values), DGATE (FP32, a row of cols values for each of
  * GATE's, leading dimension lddg); the last three are summed in a fixed order, in
  * the workspace that sgemm_block_norm_bwd_plan reports (16-byte aligned; none is
- * needed if none of them is given).  DW_post needs W_post, DGATE needs GATE.
+ * needed if none of them is given; calls that share one must not run at once).  DW_post needs W_post, DGATE needs GATE.
  * DX may be DY, DH or (kept = 0) H itself, and DO may be DY, DH or (kept = 0) O
  * itself, with the same pointer and leading dimension; other overlaps are
  * SGEMM_ERR_ALIAS.  rows == 0: DW and DW_post are set to 0.

@@ -13,7 +13,7 @@
 // Bound by memory: 16384 x 4096 bf16, h and o in 8 bits, 8 gates 131 us with the second
 // kernel (6.5 us of them), 5.2 TB/s; from 238 with rows taken in runs and their loads not
 // requested ahead.  Rows of 4095 148 (183 from bf16), 4096 x 16384 239: there the sums of a
-// lane's columns no longer fit its registers.  1000 x 1017 fp32 16.2, two launches.
+// lane's columns no longer fit its registers.  1000 x 1017 fp32 14.1, two launches.
 #pragma once
 #include "norm_internal.h"
 #include "norm_rows.h"

@@ -95,6 +95,8 @@ __global__ __launch_bounds__(COLS *STRIPS) void block_norm_sums_kernel(BlockNorm
 }
 
 // 8 wavefronts per CU (16384 x 4096 bf16 141 us, with 16 156), 16 of rows that take them.
+// Past one workgroup to a CU each takes four rows at least: the second kernel adds fewer sums
+// (1000 x 1017 fp32 17.5 us with one row each, 15.5 with four, 2000 x 1017 bf16 17.3 / 16.0).
 // Up to a quarter as many gates as workgroups get a team each, of equal size.
 struct Walkers {
     int64_t rows, gate_rows;
@@ -104,7 +106,8 @@ struct Walkers {
         constexpr int64_t ROWS = NT / L, MOST = std::max(256 * 512 / NT, 256);
         const int64_t gates = ceil_div(rows, gate_rows);
         if (gates <= MOST / 4) {
-            out->team = std::min(MOST / gates, ceil_div(gate_rows, ROWS));
+            const int64_t most = std::min(MOST, std::max<int64_t>(256, ceil_div(rows, 4 * ROWS)));
+            out->team = std::min(std::max<int64_t>(most / gates, 1), ceil_div(gate_rows, ROWS));
             out->groups = gates * out->team;
             out->parts = (gates > 1 ? 3 : 2) * out->groups;
         } else {

@@ -3,6 +3,8 @@
 #include "api_checks.h"
 #include "norm_internal.h"
 
+#include <algorithm>
+
 using namespace sgemm;
 
 namespace {
@@ -119,8 +121,10 @@ int sgemm_block_norm_bwd_plan(int64_t rows, int64_t cols, int64_t gate_rows, int
 {
     if (!dim_ok(rows) || cols < 0 || cols > SGEMM_RMSNORM_MAX_COLS || gate_rows < 0)
         return SGEMM_ERR_INVALID_VALUE;
+    // A call that reads its gate for no output sums as one without a gate, which can be more
+    // arrays: 129 to 256 gates of 513 to 1024 columns have a workgroup each.
     if (workspace_bytes)
-        *workspace_bytes = block_norm_sums(rows, cols, gate_rows).parts * cols * 4;
+        *workspace_bytes = std::max(block_norm_sums(rows, cols, gate_rows).parts, block_norm_sums(rows, cols, 0).parts) * cols * 4;
     return SGEMM_OK;
 }
 

@@ -88,8 +88,8 @@ int sgemm_block_norm_bwd(int type, int w_type, int64_t rows, int64_t cols, const
                          float *DW_post, float *DGATE, int64_t lddg, void *workspace, int64_t workspace_bytes,
                          void *stream);
 
-/* Host-only query: the workspace bytes that call needs for its sums.  gate_rows:
- * as there; rows (or 0) without a gate. */
+/* Host-only query: the workspace bytes that serve that call, whichever of its outputs
+ * are given.  gate_rows: as there; rows (or 0) without a gate. */
 int sgemm_block_norm_bwd_plan(int64_t rows, int64_t cols, int64_t gate_rows, int64_t *workspace_bytes);
 
 #ifdef __cplusplus

@@ -43,9 +43,9 @@ __device__ __forceinline__ float column_sum(const float *from, int64_t step, int
 }
 
 // COLS columns per workgroup.  blockIdx.y: 0 dw; 1 dw_post; from 2 on the gates whose sums
-// several workgroups or walkers left, `gates` of them to be looked at: with teams and where a
-// gate has at least as many rows as a walker takes all gates, else by the walker in whose
-// last row one is.
+// several workgroups or walkers left, `gates` of them to be looked at
+// (block_norm_gates_to_join): with teams and where a gate has more rows than a walker takes
+// all gates, else by the walker in whose last row one is.
 template <typename T, int COLS, int STRIPS>
 __global__ __launch_bounds__(COLS *STRIPS) void block_norm_sums_kernel(BlockNormBwdArgs g, int gates)
 {
@@ -77,7 +77,7 @@ __global__ __launch_bounds__(COLS *STRIPS) void block_norm_sums_kernel(BlockNorm
                 continue;
             }
             const float *slots = second + (int64_t)g.groups * g.cols;
-            const bool by_gate = g.gate_rows >= g.chunk;
+            const bool by_gate = g.gate_rows > g.chunk;
             const int64_t last = min<int64_t>(g.rows, (int64_t)(i + 1) * g.chunk) - 1;  // of walker i
             const int64_t gr = by_gate ? i : last / g.gate_rows;
             const int64_t first = gr * g.gate_rows, end = min<int64_t>(g.rows, first + g.gate_rows);
@@ -157,11 +157,9 @@ hipError_t launch_block_norm_bwd(BlockNormBwdArgs a, int type, bool kept, hipStr
         if (e != hipSuccess)
             return e;
     }
-    if (!a.DW && !a.DWP && !a.DG)
+    const int64_t gates = a.DG ? block_norm_gates_to_join(n, a.rows, a.gate_rows) : 0;
+    if (!a.DW && !a.DWP && gates == 0)
         return hipSuccess;
-    int64_t gates = 0;
-    if (a.DG)
-        gates = n.team || a.gate_rows >= n.chunk ? ceil_div(a.rows, a.gate_rows) : n.chunk % a.gate_rows ? n.walkers : 0;
     if (type == SGEMM_TYPE_F32)
         launch_sums<float>(a, (int)gates, s);
     else if (type == SGEMM_TYPE_FP16)

@@ -45,6 +45,15 @@ struct BlockNormSums {
     int64_t parts = 0;      // arrays of cols floats in the workspace
 };
 BlockNormSums block_norm_sums(int64_t rows, int64_t cols, int64_t gate_rows);
+// Gates that the second kernel looks at, of those whose sums are wanted: with teams all; else
+// none where every gate lies in one walker's rows, all of those longer than a walker's rows, or
+// for each walker the one that its last row belongs to.
+inline int64_t block_norm_gates_to_join(const BlockNormSums &n, int64_t rows, int64_t gate_rows)
+{
+    if (!n.team && n.chunk % gate_rows == 0)
+        return 0;
+    return n.team || gate_rows > n.chunk ? ceil_div(rows, gate_rows) : n.walkers;
+}
 hipError_t launch_block_norm_bwd(BlockNormBwdArgs a, int type, bool kept, hipStream_t s);
 
 }  // namespace sgemm

@@ -25,6 +25,9 @@ bool overlaps(const Operand (&out)[NO], const Operand (&in)[NI], const unsigned 
     return false;
 }
 
+// (a gate for all rows has 0 where there are none)
+bool gate_rows_ok(int64_t gate_rows, int64_t rows) { return gate_rows >= (rows > 0 ? 1 : 0); }
+
 Operand vector(const void *p, int64_t n, int size) { return Operand{p, 1, n, n > 1 ? n : 1, size}; }
 
 }  // namespace
@@ -45,9 +48,9 @@ int sgemm_block_norm(int type, int w_type, int64_t rows, int64_t cols, const voi
         W_post = GATE = O8 = nullptr;
     if (!W_post)
         rstd_post = nullptr;
-    if (GATE && gate_rows < 1)
+    if (GATE && !gate_rows_ok(gate_rows, rows))
         return SGEMM_ERR_INVALID_VALUE;
-    if (!GATE || gate_rows > rows)
+    if (!GATE || gate_rows > rows || rows == 0)
         gate_rows = rows > 0 ? rows : 1;
     const int size = type_bytes(type), w_size = type_bytes(w_type);
     const bool q_i8 = q_format == SGEMM_Q_I8;
@@ -138,7 +141,7 @@ int sgemm_block_norm_bwd(int type, int w_type, int64_t rows, int64_t cols, const
 {
     if (!known_type(type) || (w_type != type && w_type != SGEMM_TYPE_F32) || !dim_ok(rows) || cols < 0 ||
         cols > SGEMM_RMSNORM_MAX_COLS || (kept != 0 && kept != 1) || workspace_bytes < 0 || !std::isfinite(alpha) ||
-        (GATE && gate_rows < 1))
+        (GATE && !gate_rows_ok(gate_rows, rows)))
         return SGEMM_ERR_INVALID_VALUE;
     // (operands without rows may be NULL)
     if (rows > 0 && cols > 0 &&

@@ -315,16 +315,16 @@ Gate gate_of(PyObject *o, PyObject *gate_rows, int64_t rows, int64_t cols, int d
     w.take("gate", g.m.kind);
     if (given(gate_rows)) {
         g.rows = integer(gate_rows);
-    } else {
+    } else if (rows > 0) {
         if (g.m.rows == 0 || rows % g.m.rows != 0)
             refuse(PyExc_ValueError, "%lld rows do not divide among %lld rows of gate: gate_rows is needed", (long long)rows,
                    (long long)g.m.rows);
-        g.rows = rows / g.m.rows > 0 ? rows / g.m.rows : 1;
+        g.rows = rows / g.m.rows;
     }
-    if (g.rows < 1)
+    if (g.rows < (rows > 0 ? 1 : 0))
         refuse(PyExc_ValueError, "gate_rows must be positive");
-    const int64_t gates = rows / g.rows + (rows % g.rows != 0);
-    if (g.m.cols != cols || (rows > 0 && g.m.rows != gates))
+    const int64_t gates = rows > 0 ? rows / g.rows + (rows % g.rows != 0) : g.m.rows;
+    if (g.m.cols != cols || g.m.rows != gates)
         refuse(PyExc_ValueError, "gate has shape (%lld, %lld), not (%lld, %lld)", (long long)g.m.rows, (long long)g.m.cols,
                (long long)gates, (long long)cols);
     return g;
@@ -440,10 +440,15 @@ PyObject *block_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
         }
         const Lent w = workspace(a[18], d);
         return launch(d, a[19], [&](void *s) {
-            return block_norm_bwd_fn(kind, wt.kind, rows, cols, DY.p, DY.ld, DH.p, DH.ld, h8 || o8, H.q.p, H.q.ld, H.scales(),
-                                     H.s.ld, O.q.p, O.q.ld, O.scales(), O.s.ld, W, WP, rstd, rstd_post, G.m.p, G.m.ld, G.rows,
-                                     alpha, DX.p, DX.ld, DO.p, DO.ld, DW, DWP, static_cast<float *>(DG.p), DG.ld, w.p, w.bytes,
-                                     s);
+            const int status = block_norm_bwd_fn(
+                kind, wt.kind, rows, cols, DY.p, DY.ld, DH.p, DH.ld, h8 || o8, H.q.p, H.q.ld, H.scales(), H.s.ld, O.q.p,
+                O.q.ld, O.scales(), O.s.ld, W, WP, rstd, rstd_post, G.m.p, G.m.ld, G.rows, alpha, DX.p, DX.ld, DO.p, DO.ld, DW,
+                DWP, static_cast<float *>(DG.p), DG.ld, w.p, w.bytes, s);
+            // gates without rows: the C function knows of none, their sums are 0
+            if (status == SGEMM_OK && rows == 0 && cols > 0 && DG.rows > 0)
+                return i8_gemm_fn(SGEMM_TYPE_F32, DG.rows, cols, 0, 0.0f, nullptr, 1, nullptr, nullptr, 1, nullptr, 0.0f, DG.p,
+                                  DG.ld, nullptr, 0, s);
+            return status;
         });
     });
 }

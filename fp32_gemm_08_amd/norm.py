@@ -75,7 +75,7 @@ def block_norm(X, O, W, eps=1e-6, w_post=None, gate=None, gate_rows=None, alpha=
     X (the residual stream), O (the block's output; None: no block), H and Y are
     (rows, cols) of one type (float32, float16 or bfloat16); W and w_post (cols) and
     gate (cols, or a row of cols for every ``gate_rows`` rows of X; by default the rows
-    divide evenly) are of that type or float32.  w_post None: z = O; gate None: 1.
+    divide evenly; where X has none, of any number) are of that type or float32.  w_post None: z = O; gate None: 1.
     norm(v) = v / sqrt(mean(v^2) + eps), row by row.  Written where given: H <- h (may
     be X or O itself), Y <- y, Q with S <- y in 8 bits (float8_e4m3fn with S
     (ceil(cols/128), rows), or int8 with S (rows)), H8 with SH and O8 with SO <- h and O
@@ -96,10 +96,10 @@ def block_norm_backward(dY, H, O, W, rstd, dX, dO, SH=None, SO=None, w_post=None
     dY is the gradient of y (None: nothing reaches it, and H, W and rstd are not
     needed), dH what reaches h along the residual path (or None).  H and O are what
     the forward pass kept: both of dY's type, or both float8_e4m3fn with their scales
-    SH and SO; O is needed for dGate, or with w_post, and may be None elsewhere.  dX and dO (either may be None) may be dY
-    or dH, and H and O themselves where those are of dY's type.  dW and dW_post (cols)
-    and dGate (gate's shape) are float32, or None, and need a ``workspace`` of
-    sgemm_block_norm_bwd_plan's bytes.
+    SH and SO; O is needed for dGate, or with w_post, and may be None elsewhere.  dX and dO
+    (either may be None) may be dY or dH, and H and O themselves where those are of dY's
+    type.  dW and dW_post (cols) and dGate (gate's shape) are float32, or None, and need a
+    ``workspace`` of sgemm_block_norm_bwd_plan's bytes; without rows they are set to 0.
     """
     check(tensors().block_norm_backward(dY, H, O, W, rstd, dX, dO, SH, SO, w_post, rstd_post, gate, gate_rows, alpha, dH, dW,
                                         dW_post, dGate, workspace, stream))

@@ -32,7 +32,8 @@ extern "C" {
  * X, O, H and Y are rows x cols of `type`; W, W_post (cols values) and GATE are
  * of w_type (`type` or FP32).  GATE has ceil(rows/gate_rows) rows of cols values,
  * row i of x takes row i / gate_rows of it (gate_rows = rows: a gate per
- * channel; a sequence's length: one for each sequence; 1: one for each token).
+ * channel; a sequence's length: one for each sequence; 1: one for each token); it is at
+ * least 1, or 0 where rows is.
  *   O NULL:      no block: h = alpha * x (W_post, GATE, O8 and rstd_post are ignored)
  *   W_post NULL: no norm after the block: z = o (rstd_post is then not written)
  *   GATE NULL:   gate 1 (gate_rows and ldg are ignored)

@@ -5,12 +5,14 @@ nanoseconds.  It is built next to the library; there is no other way to these ca
 from __future__ import annotations
 
 import ctypes
+import os
 
 from .sgemm import SGEMM_OK, SgemmError, load, sgemm_f32_status_string
 
 # The C functions it calls, in the order of its bind().
 CALLS = ("sgemm_i8_gemm", "sgemm_i8_quantize", "sgemm_f8_requantize", "sgemm_block_norm", "sgemm_block_norm_bwd")
 
+MODULE = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_tensors.so")
 _module = None
 
 
@@ -26,6 +28,9 @@ def _bind():
     try:
         from . import _tensors
     except ImportError as e:
+        if os.path.exists(MODULE):
+            raise RuntimeError(f"_tensors.so does not load ({e}): it is built for one Python and one torch; build it again "
+                               "(python -m fp32_gemm_08_amd.build)") from e
         raise RuntimeError("_tensors.so is missing: build it (python -m fp32_gemm_08_amd.build)") from e
     lib = load()
     _tensors.bind(tuple(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in CALLS),

@@ -60,8 +60,9 @@ __device__ __forceinline__ void f8_wait_barrier()
     asm volatile("s_barrier" ::: "memory");
 }
 
-// What a wavefront loads of each stage.
-template <class G, int S, bool ROWB, bool LATE>
+// What a wavefront loads of each stage.  SCALED: the stages have scales; without, Args are
+// another family's with the same operands.
+template <class G, int S, bool ROWB, bool LATE, bool SCALED = true>
 struct F8Stages {
     typedef F8Pipe<G, S, ROWB, LATE> P;
     uint8_t *smem;
@@ -88,7 +89,8 @@ struct F8Stages {
     uint32_t soff, sblock;
     int nk, tail;                   // stages, values of the last stage's rows
 
-    __device__ __forceinline__ F8Stages(const F8GemmArgs &g, uint8_t *lds, int m0, int n0, int w, int split)
+    template <class Args>
+    __device__ __forceinline__ F8Stages(const Args &g, uint8_t *lds, int m0, int n0, int w, int split)
         : smem(lds)
     {
         const int lane = threadIdx.x & 63;
@@ -116,22 +118,24 @@ struct F8Stages {
 #pragma unroll
         for (int x = 0; x < 2; ++x)
             past[x] = 16 * ((lane & 7) ^ f8_swz(8 * (w * G::LOADS + x) + lane / 8)) >= tail;
-        sblock = w % P::NSC;
-        const int si = 64 * sblock + lane;
-        if (64 * (int)sblock < G::BM) {
-            sbase = g.SA + m0;
-            sstep = g.ldsa;
-            soff = 4u * (uint32_t)min(si / G::WM * G::WM + 16 * (si % G::FM) + si % G::WM / G::FM, g.M - 1 - m0);
-        } else if constexpr (ROWB) {
-            sbase = g.SB + n0;
-            sstep = g.ldsb;
-            soff = 4u * (uint32_t)min(si - G::BM, g.N - 1 - n0);
-        } else {
-            sbase = g.SB + (int64_t)(n0 / 128) * g.ldsb;
-            sstep = 1;
-            soff = 4u * (uint32_t)(min(n0 + 4 * (si - G::BM), g.N - 1) / 128 - n0 / 128) * (uint32_t)g.ldsb;
+        if constexpr (SCALED) {
+            sblock = w % P::NSC;
+            const int si = 64 * sblock + lane;
+            if (64 * (int)sblock < G::BM) {
+                sbase = g.SA + m0;
+                sstep = g.ldsa;
+                soff = 4u * (uint32_t)min(si / G::WM * G::WM + 16 * (si % G::FM) + si % G::WM / G::FM, g.M - 1 - m0);
+            } else if constexpr (ROWB) {
+                sbase = g.SB + n0;
+                sstep = g.ldsb;
+                soff = 4u * (uint32_t)min(si - G::BM, g.N - 1 - n0);
+            } else {
+                sbase = g.SB + (int64_t)(n0 / 128) * g.ldsb;
+                sstep = 1;
+                soff = 4u * (uint32_t)(min(n0 + 4 * (si - G::BM), g.N - 1) / 128 - n0 / 128) * (uint32_t)g.ldsb;
+            }
+            sbase += first * sstep;
         }
-        sbase += first * sstep;
     }
     __device__ __forceinline__ uint8_t *stage(int kb) const { return smem + (kb % S) * P::STAGE; }
     __device__ __forceinline__ uint8_t *scales(int kb) const
@@ -142,7 +146,7 @@ struct F8Stages {
     // zeros, so that every step makes the same loads.
     __device__ __forceinline__ void fetch(int kb, int w, int j) const
     {
-        if (j == G::LOADS)
+        if (SCALED && j == G::LOADS)
             f8_load_lds4(sbase + kb * sstep, kb < nk ? F8_ALL : 0, soff, scales(kb) + 256 * sblock);
         else {
             const bool second = FEW && MIXED && 8 * (w * G::LOADS + j) >= G::BM;

@@ -6,22 +6,16 @@
 
 namespace sgemm {
 
-// Blocks of MB x MB elements of C.  The instructions take rows of B as their first operand
-// and rows of A as their second: lane l holds row m = l % MB of C, and of its columns groups
-// of 4 consecutive ones, the first at 4 * (l / MB), each next one 256 / MB further.  Lane l
-// supplies of row l % MB of each operand 16 consecutive values for a slice of 1024 / MB
-// values of k, at chunk l / MB of the slice (which place is free as long as both agree).
-template <int MB> struct I8Block;
-template <> struct I8Block<16> {
-    typedef f8_i32x4 Acc;
-    static __device__ __forceinline__ Acc mma(f8_i32x4 b, f8_i32x4 a, Acc c)
-    {
-        return __builtin_amdgcn_mfma_i32_16x16x64_i8(b, a, c, 0, 0, 0);
-    }
-};
-template <int MB> struct I8Frag {
-    static constexpr int NS = MB / 8;           // slices of a k-block of 128
-    f8_i32x4 v[NS];
+// Blocks of 16 x 16 elements of C.  The instruction takes rows of B as its first operand and
+// rows of A as its second: lane l holds row m = l % 16 of C, columns 4 * (l / 16) .. +3.  Lane l
+// supplies of row l % 16 of each operand 16 consecutive values for a slice of 64 values of k,
+// at chunk l / 16 of the slice (which place is free as long as both agree).
+__device__ __forceinline__ f8_i32x4 i8_mma(f8_i32x4 b, f8_i32x4 a, f8_i32x4 c)
+{
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(b, a, c, 0, 0, 0);
+}
+struct I8Frag {
+    f8_i32x4 v[2];                              // slices of a k-block of 128
 };
 
 // Columns n .. n+7 of row m of C <- alpha * (v * sa) * sb + beta * C.
@@ -64,9 +58,9 @@ __device__ __forceinline__ void i8_put_part(int *row, int n, int cols, const int
 
 // The scales of what a lane writes of its wavefront's FM x FN blocks from (m, n) on, requested
 // before the products: at their end the latency of a first access would be the kernel's.
-template <int MB, int FM, int FN> struct I8Scales {
-    static constexpr int LANES = MB * FN / 8, TURNS = MB * LANES / 64;  // lanes of a row; rows of a lane in a block
-    static_assert(64 % LANES == 0 && TURNS * 64 == MB * LANES, "whole turns of the lanes");
+template <int FM, int FN> struct I8Scales {
+    static constexpr int LANES = 2 * FN, TURNS = FN / 2;        // lanes of a row; rows of a lane in a block
+    static_assert(64 % LANES == 0 && TURNS * 64 == 16 * LANES, "whole turns of the lanes");
     float sa[FM][TURNS], sb[8];
     __device__ __forceinline__ I8Scales(const I8GemmArgs &g, int m, int n)
     {
@@ -76,28 +70,24 @@ template <int MB, int FM, int FN> struct I8Scales {
         for (int i = 0; i < FM; ++i)
 #pragma unroll
             for (int t = 0; t < TURNS; ++t)
-                sa[i][t] = g.SA[min(m + MB * i + lane / LANES + t * (64 / LANES), g.M - 1)];
+                sa[i][t] = g.SA[min(m + 16 * i + lane / LANES + t * (64 / LANES), g.M - 1)];
     }
 };
 
-// A wavefront's MB rows of FN blocks of C, block row i, through `buf` (MB x (MB FN + 4) words
+// A wavefront's 16 rows of FN blocks of C, block row i, through `buf` (16 x (16 FN + 4) words
 // of this wavefront's own), so that the lanes of a row write it together.  `part`: this
 // split's partial sums.
-template <int MB, int FM, int FN>
-__device__ __forceinline__ void i8_store_rows(const I8GemmArgs &g, int *buf, int m, int n, int i,
-                                              const typename I8Block<MB>::Acc (&acc)[FN], const I8Scales<MB, FM, FN> &sc,
-                                              int *part = nullptr)
+template <int FM, int FN>
+__device__ __forceinline__ void i8_store_rows(const I8GemmArgs &g, int *buf, int m, int n, int i, const f8_i32x4 (&acc)[FN],
+                                              const I8Scales<FM, FN> &sc, int *part = nullptr)
 {
-    constexpr int PITCH = MB * FN + 4, LANES = MB * FN / 8;
+    constexpr int PITCH = 16 * FN + 4, LANES = 2 * FN;
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int j = 0; j < FN; ++j)
+        *reinterpret_cast<f8_i32x4 *>(buf + lane % 16 * PITCH + 16 * j + 4 * (lane / 16)) = acc[j];
 #pragma unroll
-        for (int x = 0; x < MB * MB / 256; ++x)
-            *reinterpret_cast<f8_i32x4 *>(buf + lane % MB * PITCH + MB * j + 4 * (lane / MB) + 256 / MB * x) =
-                f8_i32x4{acc[j][4 * x], acc[j][4 * x + 1], acc[j][4 * x + 2], acc[j][4 * x + 3]};
-#pragma unroll
-    for (int t = 0; t < I8Scales<MB, FM, FN>::TURNS; ++t) {
+    for (int t = 0; t < I8Scales<FM, FN>::TURNS; ++t) {
         const int r = lane / LANES + t * (64 / LANES), c = 8 * (lane % LANES);
         if (m + r >= g.M || n + c >= g.N)
             continue;

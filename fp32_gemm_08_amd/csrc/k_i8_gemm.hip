@@ -29,7 +29,7 @@ __global__ __launch_bounds__(G::NT *GROUPS) void i8_tile_kernel(I8GemmArgs g)
     const int wm = w / G::WGN, wn = w % G::WGN;
     uint8_t *const st = smem + group * G::STAGE;
 
-    const I8Scales<16, G::FM, G::FN> scales(g, m0 + wm * G::WM, n0 + wn * G::WN);
+    const I8Scales<G::FM, G::FN> scales(g, m0 + wm * G::WM, n0 + wn * G::WN);
     f8_i32x4 acc[G::FM][G::FN];
 #pragma unroll
     for (int i = 0; i < G::FM; ++i)
@@ -92,7 +92,7 @@ __global__ __launch_bounds__(G::NT *GROUPS) void i8_tile_kernel(I8GemmArgs g)
                     const f8_i32x4 a = read(wm * G::WM + 16 * i + l16, q + 4 * half);
 #pragma unroll
                     for (int j = 0; j < G::FN; ++j)
-                        acc[i][j] = I8Block<16>::mma(b[j], a, acc[i][j]);
+                        acc[i][j] = i8_mma(b[j], a, acc[i][j]);
                 }
             }
         }
@@ -120,7 +120,7 @@ __global__ __launch_bounds__(G::NT *GROUPS) void i8_tile_kernel(I8GemmArgs g)
     static_assert((GROUPS - 1) * SUMS + G::NW * G::OUT * 4 <= GROUPS * G::STAGE, "LDS size");
 #pragma unroll
     for (int i = 0; i < G::FM; ++i)
-        i8_store_rows<16, G::FM, G::FN>(g, buf, m0 + wm * G::WM + 16 * i, n0 + wn * G::WN, i, acc[i], scales);
+        i8_store_rows<G::FM, G::FN>(g, buf, m0 + wm * G::WM + 16 * i, n0 + wn * G::WN, i, acc[i], scales);
 }
 
 // C from the splits' partial sums, which are integers: their order does not matter.

@@ -114,8 +114,8 @@ __global__ __launch_bounds__(512) void i8_skinny_kernel(I8GemmArgs g)
             for (int i = 0; i < FM; ++i)
 #pragma unroll
                 for (int j = 0; j < FN; ++j) {
-                    acc[i][j] = I8Block<16>::mma(b.lo[FM + j], b.lo[i], acc[i][j]);
-                    acc[i][j] = I8Block<16>::mma(b.hi[FM + j], b.hi[i], acc[i][j]);
+                    acc[i][j] = i8_mma(b.lo[FM + j], b.lo[i], acc[i][j]);
+                    acc[i][j] = i8_mma(b.hi[FM + j], b.hi[i], acc[i][j]);
                 }
             if (kb + DEPTH * NW < nk)
                 load(b, kb + DEPTH * NW);

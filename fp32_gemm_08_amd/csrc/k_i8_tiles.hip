@@ -11,16 +11,16 @@ hipError_t launch_i8_tile(const I8GemmArgs &a, int kid, int splits, hipStream_t 
     const unsigned grid = (unsigned)((int64_t)a.tiles_m * a.tiles_n * splits);
     switch (kid) {
     case KID_I8_S:
-        i8_flat_kernel<F8Geo<64, 64, 2, 2>, 4, 16><<<grid, 256, 0, s>>>(a);
+        i8_flat_kernel<F8Geo<64, 64, 2, 2>, 4><<<grid, 256, 0, s>>>(a);
         break;
     case KID_I8_N:
-        i8_flat_kernel<F8Geo<128, 64, 4, 2>, 6, 16><<<grid, 512, 0, s>>>(a);
+        i8_flat_kernel<F8Geo<128, 64, 4, 2>, 6><<<grid, 512, 0, s>>>(a);
         break;
     case KID_I8_M:
-        i8_flat_kernel<F8Geo<128, 128, 2, 4>, 4, 16><<<grid, 512, 0, s>>>(a);
+        i8_flat_kernel<F8Geo<128, 128, 2, 4>, 4><<<grid, 512, 0, s>>>(a);
         break;
     default:
-        i8_pipe_kernel<F8Geo<256, 256, 2, 4>, 2, 16><<<grid, 512, 0, s>>>(a);
+        i8_pipe_kernel<F8Geo<256, 256, 2, 4>, 2><<<grid, 512, 0, s>>>(a);
         break;
     }
     return hipGetLastError();

@@ -10,10 +10,12 @@
 // that hold a row) takes rows one after another and keeps its columns' sums; a second kernel
 // adds what the workgroups left, in a fixed order.
 //
-// Bound by memory: 16384 x 4096 bf16, h and o in 8 bits, 8 gates 131 us with the second
-// kernel (6.5 us of them), 5.2 TB/s; from 238 with rows taken in runs and their loads not
-// requested ahead.  Rows of 4095 148 (183 from bf16), 4096 x 16384 239: there the sums of a
-// lane's columns no longer fit its registers.  1000 x 1017 fp32 14.1, two launches.
+// Bound by memory: 16384 x 4096 bf16, h and o in 8 bits, 8 gates 136 to 142 us with the second
+// kernel (6.5 us of them), 4.9 TB/s (fp16 145, fp32 229, from bf16 159, a gate for each row
+// 290); from 238 with rows taken in runs and their loads not requested ahead.  Rows of 4095 148
+// (184 from bf16).  Above 8192 columns the sums of a lane's columns no longer fit its registers:
+// 4096 x 16384 267 us, 2048 x 32768, where a row does not either, 1330.  1000 x 1017 fp32 14.0,
+// two launches.
 #pragma once
 #include "norm_internal.h"
 #include "norm_rows.h"
@@ -91,7 +93,7 @@ __device__ __forceinline__ void weights8(const void *W, int64_t at, int w_f32, i
 
 // The rows of a walker.  One gate a walker: `team` workgroups share a gate's rows and take
 // them in turn, so that all walkers of a gate are at neighbouring rows at a time (rows in
-// runs of a walker's own took 154 instead of 138 us, 16384 x 4096 bf16), and workgroups of
+// runs of a walker's own took 154 where this took 138 us, 16384 x 4096 bf16), and workgroups of
 // one XCD at the nearest, since the scales of 32 consecutive rows share a line.  SEVERAL:
 // `chunk` consecutive rows.
 template <bool SEVERAL, int ROWS> struct BlockNormWalk {
@@ -401,7 +403,7 @@ __global__ __launch_bounds__(NT) void block_norm_bwd_kernel(BlockNormBwdArgs g)
 // conditions in the loop, the next row's values requested as soon as this row's are
 // converted, and n, g, m and p kept from one pass over the row to the next.  TAIL: the row's
 // last piece may be shorter (rows of at least 8); its wavefront alone moves what it loaded
-// (as it does in the other kernel, before the next row is requested, which then waits for
+// (moved before the next row is requested, as in the other kernel, that request waits for
 // memory: 16384 x 4095 330 us).
 template <typename T, int NT, int L, bool KEPT, bool POST, bool TAIL>
 __global__ __launch_bounds__(NT) void block_norm_bwd_all_kernel(BlockNormBwdArgs g)

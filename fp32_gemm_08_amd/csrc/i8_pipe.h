@@ -23,10 +23,10 @@ struct I8Pipe {
 // is requested into its place, and the next stage's fragments are read under the last row's
 // products.
 //
-// Bound by the matrix cores at the clock that power leaves them: 8192^3 to bf16 419 us,
-// 2.62 Pop/s, from 944 with a tile that goes through registers into the LDS; the cores are
-// busy 57 to 61% of the cycles at 1.76 to 1.97 GHz.  Operands of zeros take 405 us, operands
-// that stay in the L2 336 to 357.
+// Bound by the loads: 8192^3 to bf16 takes 417 to 426 us, 2.6 Pop/s (944 with a tile that goes
+// through registers into the LDS), operands that stay in the L2 336 to 357, and operands of
+// zeros, which draw less power, still 405; the matrix cores are busy 57 to 61% of the cycles,
+// at 1.76 GHz in long runs and 1.97 in short ones.
 template <class G, int S>
 __global__ __launch_bounds__(G::NT) void i8_pipe_kernel(I8GemmArgs g)
 {
@@ -129,8 +129,8 @@ __global__ __launch_bounds__(G::NT) void i8_pipe_kernel(I8GemmArgs g)
 // The same for tiles of few blocks a wavefront: all fragments of the next stage are read
 // before this stage's products, into a second set of registers.  The wavefronts meet once a
 // step, when each has its set: the stage S ahead is requested into the place of the one in
-// the registers.  64 x 16384 x 4096 from memory 17.9 us (3.9 TB/s of B's bytes; 13.2 with B
-// still in the cache behind the L2), 23.7 on the tile that goes through registers.
+// the registers.  64 x 16384 x 4096 from memory 17.9 us (3.9 TB/s of B's bytes); with B still
+// in the cache behind the L2 13.2, 15.7 on the tile that goes through registers.
 template <class G, int S>
 __global__ __launch_bounds__(G::NT) void i8_flat_kernel(I8GemmArgs g)
 {

@@ -6,10 +6,11 @@
 // its mean square, h for its own, and y, where it is quantised with one scale for the
 // row, for its largest value.
 //
-// Bound by memory: 16384 x 4096 bf16 with h, y in 8 bits and both kept copies 127 us, 4.8 TB/s of its
-// 611 MB, more than half of them written; 8192 x 8192 128, 4096 x 16384 139, packed rows of
-// 4095 154.  A row in registers from its first read to its last output is what keeps it to
-// one pass.  One row 5.3 us: a trip to memory, two sums over the workgroup and the launch.
+// Bound by memory: 16384 x 4096 bf16 with h, y in 8 bits and both kept copies 119 to 121 us, 5.1
+// TB/s of its 611 MB, more than half of them written (fp16 121, fp32 217); with h and y in 8-bit
+// integers alone 88, 5.3 TB/s; 8192 x 8192 128, 4096 x 16384 144, 2048 x 32768 137, packed rows
+// of 4095 153.  A row in registers from its first read to its last output is what keeps it to
+// one pass.  One row 5.1 us: a trip to memory, two sums over the workgroup and the launch.
 #include "norm_internal.h"
 #include "norm_rows.h"
 

@@ -94,9 +94,10 @@ __global__ __launch_bounds__(COLS *STRIPS) void block_norm_sums_kernel(BlockNorm
     }
 }
 
-// 8 wavefronts per CU (16384 x 4096 bf16 141 us, with 16 156), 16 of rows that take them.
-// Past one workgroup to a CU each takes four rows at least: the second kernel adds fewer sums
-// (1000 x 1017 fp32 17.5 us with one row each, 15.5 with four, 2000 x 1017 bf16 17.3 / 16.0).
+// 8 wavefronts per CU (8 / 16: 16384 x 4096 bf16 142 / 144 us, 16384 x 1000 43.5 / 49.4), 16 of
+// rows that take them.  Past one workgroup to a CU each takes four rows at least: the second
+// kernel adds fewer sums (one row / two / four / eight: 1000 x 1017 fp32 15.7 / 13.8 / 14.0 /
+// 14.0 us, 2000 x 1017 19.0 / 18.7 / 17.2 / 19.2, 1000 x 2000 16.2 / 16.1 / 14.8 / 14.8).
 // Up to a quarter as many gates as workgroups get a team each, of equal size.
 struct Walkers {
     int64_t rows, gate_rows;
@@ -120,7 +121,8 @@ struct Walkers {
 };
 
 // Of up to 256 arrays 8 strips of 64 columns, else 32 of 32 columns: the former are a quarter
-// of the wavefronts (256 arrays of 4096 columns and 8 gates 15.3 us with 32 strips).
+// of the wavefronts (8 / 32 strips, both kernels: 16384 x 4096 with 8 gates, 256 arrays, 142 /
+// 150 us, 16384 x 1000, 1024 arrays, 44.7 / 43.5).
 template <typename T> void launch_sums(const BlockNormBwdArgs &a, int gates, hipStream_t s)
 {
     const unsigned y = (unsigned)(2 + std::min(gates, 64));

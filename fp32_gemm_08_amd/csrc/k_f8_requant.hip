@@ -10,8 +10,8 @@
 // ends with the complete maximum of one and divides for one; the factors come back the same
 // way.  No barrier, and the LDS's crossbar only for the order in which lanes write.
 //
-// Bound by memory: 16384 x 4096 25.6 us, 5.4 TB/s (as an input of k_f8_quant.hip, a 128 x 128
-// tile through the LDS, 45.1).  Without the swap of lanes before the stores, whose
+// Bound by memory: 16384 x 4096 23.5 to 25.6 us, 5.9 TB/s (as an input of k_f8_quant.hip, a 128
+// x 128 tile through the LDS, 45.1).  Without the swap of lanes before the stores, whose
 // neighbouring lanes then write to different lines, 37.4; with the loads past the L2 too, which
 // a line's two halves meet in, 47.4 with a wavefront a workgroup.
 #include "f8_types.h"
@@ -196,8 +196,8 @@ void launch_tiles(F8QuantArgs a, int format_x, int format, hipStream_t s)
 }  // namespace
 
 // Tiles beside each other share lines of the rows: 4 of them a workgroup where that fills the
-// CUs, else 2 (2 / 4: 8192 x 16384 75.3 / 67.1 us, 16384 x 4097 packed 35.3 / 28.9, 1000 x 1017
-// packed 7.0 / 7.6).
+// CUs, else 2 (2 / 4: 8192 x 16384 75.8 / 67.3 us, 16384 x 4097 packed 35.1 / 29.1, 1000 x 1017
+// packed 7.1 / 7.6).
 hipError_t launch_f8_requantize(const F8QuantArgs &a, int format_x, int format, hipStream_t s)
 {
     if (((int64_t)a.rows + 127) / 128 * (((int64_t)a.cols + 255) / 256) >= 256)

@@ -12,9 +12,11 @@ namespace {
 // next one is requested before it is multiplied.  GROUPS times G::NW wavefronts take the
 // k-blocks in turn, each group in a stage of its own; their sums meet in the LDS.
 //
-// 1000 x 1017 x 999 packed 9.2 us, 8 k-blocks: about 10 bytes per CU and cycle however they
-// are loaded (requested 2 or 4 blocks ahead 10.4 to 11.1, two blocks a step 10.4, in words of
-// 4 bytes 15.2): a row's 128 bytes lie in two lines, which the next block needs again.
+// 1000 x 1017 x 999 packed 9.1 us, 8 k-blocks: about 10 bytes per CU and cycle however they
+// are loaded (one group and operands from memory 11.6; requested 2 or 4 blocks ahead then 10.4
+// to 11.1, two blocks a step 10.4, whole lines shifted in registers 12.2, in words of 4 bytes
+// 15.2, and four groups 10.2): a row's 128 bytes lie in two lines, which the next block needs
+// again.
 template <class G, int GROUPS>
 __global__ __launch_bounds__(G::NT *GROUPS) void i8_tile_kernel(I8GemmArgs g)
 {
@@ -146,9 +148,10 @@ __global__ __launch_bounds__(256) void i8_join_kernel(I8GemmArgs g, int splits)
 
 typedef F8Geo<64, 64, 2, 2> GS;
 // Groups of wavefronts to a workgroup for rows at any alignment: with no more than one tile to
-// a CU, four (1 / 4: 1000 x 1017 x 999 11.6 / 10.2 us, 20 x 8001 x 4001 39.5 / 28.2, 100 x 4001 x
-// 4001 38.1 / 26.6, 300 x 2000 x 5001 22.4 / 23.1); with more, other tiles' workgroups fill the
-// CU (1000 x 2001 x 1001 12.3 / 16.4, 2047^3 36.2 / 51.7).  Two were between them throughout.
+// a CU, four (1 / 2 / 4, to FP32 without a workspace: 1000 x 1017 x 999 9.9 / 9.0 / 9.1 us, 20 x
+// 8001 x 4001 31.1 / 24.1 / 21.1, 100 x 4001 x 4001 30.8 / 23.7 / 20.7, 300 x 2000 x 5001 36.5 /
+// 27.9 / 24.0); with more, other tiles' workgroups fill the CU (1000 x 2001 x 1001 12.3 / 12.3 /
+// 16.3, 2047^3 33.0 / 35.5 / 44.7).
 int any_groups(int64_t tiles) { return tiles <= 256 ? 4 : 1; }
 constexpr int64_t kMaxJoin = int64_t{64} << 20;  // bytes of partial sums a call may ask for
 
@@ -159,10 +162,16 @@ double join_us(int64_t bytes) { return 2.5 + (double)bytes * 0.5e-6; }
 //     2 us + the larger of (the rounds of workgroups that the 256 CUs take) and (2.2 us and
 //     the operands' and C's bytes at 5 TB/s) + what joining the parts takes.
 // A round of one workgroup on each CU takes (k-blocks of a part * step + ends); the 64 x 64
-// tile leaves room for two, and a round of two takes (k-blocks * step2 + ends2).  Measured
-// (bf16 C, us): 64 x 64 tiles 256 x 4096 x 4096 13.6, 512 x 4096 x 4096 19.9, 2048^3 21.1;
-// 128 x 64 512 x 4096 x 1024 8.2, x 4096 18.0; 128 x 128 2048^3 15.3, 1024 x 4096 x 4096
-// 23.9; 256 x 256 4096 x 4096 x 1024 25.1, 4096^3 63.7.
+// tile leaves room for two, and a round of two takes (k-blocks * step2 + ends2).  The constants
+// are of operands from memory; with operands in the caches the tiles take (bf16 C, us):
+//                        64 x 64   128 x 64   128 x 128   256 x 256
+//     256 x 4096 x 4096     11.6                               48.0
+//     512 x 4096 x 1024      6.6        7.1         8.5
+//     512 x 4096 x 4096     15.2       15.3        19.4        48.1
+//     2048^3                17.4       18.5        12.7        29.8
+//     1024 x 4096 x 4096               29.8        20.3        48.3
+//     4096 x 4096 x 1024                           31.0        21.2
+// and the estimate takes the fastest of each row but the third, where it is 0.1 off.
 I8GemmPlan plan_tiles(int64_t M, int64_t N, int64_t K, int64_t room, double &us)
 {
     static const struct { int kid, bm, bn, threads; double step, ends, step2, ends2; } kTiles[4] = {
@@ -193,13 +202,13 @@ I8GemmPlan plan_tiles(int64_t M, int64_t N, int64_t K, int64_t room, double &us)
 }
 
 // Up to 16 rows: 16 columns per workgroup, 32 where that still leaves two workgroups to
-// each CU (16 x 16384 x 4096 20.0 / 15.7 us, 8 x 8192 x 8192 16.2 / 19.4), k split where
-// few workgroups go through a long k (1 x 1024 x 16384 11.9 us, in 8 parts 6.8 and the join).
+// each CU (16 x 16384 x 4096 17.2 / 15.2 us, 8 x 8192 x 8192 14.5 / 18.0), k split where
+// few workgroups go through a long k (1 x 1024 x 16384 11.3 us, in 8 parts with their join 9.6).
 // Up to 32 rows the same with two blocks of rows, as long as one workgroup to a CU covers the
 // columns and A's rows, which every workgroup reads, are short (64 x 64 tiles / this: 32 x 4096
-// x 4096 10.8 / 8.5 us, 32 x 1024 x 8192 14.9 / 11.6, 17 x 500 x 1000 packed 8.6 / 4.2; but 32 x
-// 8192 x 4096 13.6 / 14.9, 32 x 4096 x 16384 21.6 / 24.7).  With four blocks 64 x 4096 x 4096
-// took 12.1 against the tiles' 12.4, 64 x 8192 x 4096 22.6 against 14.6.
+// x 4096 9.5 / 7.9 us, 32 x 1024 x 8192 12.5 / 10.9, 17 x 500 x 1000 packed 6.6 / 3.9; but 32 x
+// 8192 x 4096 11.3 / 14.1, 32 x 4096 x 16384 16.4 / 23.7).  With four blocks of rows 64 x 4096 x
+// 4096 takes 11.5 against the tiles' 10.4, 64 x 8192 x 4096 21.9 against 11.4.
 bool skinny(int64_t M, int64_t N, int64_t K) { return M <= 16 || (M <= 32 && N <= 4096 && K <= 8192); }
 int skinny_cols(int64_t N) { return N < 16384 ? 16 : 32; }
 

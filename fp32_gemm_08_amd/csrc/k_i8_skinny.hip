@@ -43,7 +43,7 @@ __device__ __forceinline__ void i8_put4(const I8GemmArgs &g, int m, int n, f8_i3
 // DEPTH k-blocks ahead.  The wavefronts' sums are added through the LDS.
 //
 // 1 x 4096 x 4096 5.3 us for 3.3 of B's bytes: a trip to memory, the join and the launch;
-// 16 x 16384 x 4096 15.7, 4.3 TB/s.
+// 16 x 16384 x 4096 15.2, 4.5 TB/s.
 template <int FM, int FN, int DEPTH>
 __global__ __launch_bounds__(512) void i8_skinny_kernel(I8GemmArgs g)
 {

@@ -3,9 +3,10 @@
 
 namespace sgemm {
 
-// Blocks of 16 x 16; with 32 x 32 ones (half the operand reads of the matrix cores) 128 x
-// 128 tiles took 38.4 against 33.3 us at 4096 x 4096 x 1024, 64 x 64 ones 45.5 against 44.0,
-// 256 x 256 ones 487 to 497 against 445 to 505 at 8192^3.
+// Blocks of 16 x 16; with 32 x 32 ones (half the operand reads of the matrix cores), measured
+// before the scales were requested ahead, 128 x 128 tiles took 38.4 against 33.3 us at 4096 x
+// 4096 x 1024, 64 x 64 ones 45.5 against 44.0, 256 x 256 ones 487 to 497 against 445 to 505 at
+// 8192^3.
 hipError_t launch_i8_tile(const I8GemmArgs &a, int kid, int splits, hipStream_t s)
 {
     const unsigned grid = (unsigned)((int64_t)a.tiles_m * a.tiles_n * splits);

@@ -75,7 +75,8 @@ def block_norm(X, O, W, eps=1e-6, w_post=None, gate=None, gate_rows=None, alpha=
     X (the residual stream), O (the block's output; None: no block), H and Y are
     (rows, cols) of one type (float32, float16 or bfloat16); W and w_post (cols) and
     gate (cols, or a row of cols for every ``gate_rows`` rows of X; by default the rows
-    divide evenly; where X has none, of any number) are of that type or float32.  w_post None: z = O; gate None: 1.
+    divide evenly; where X has none, of any number) are all of that type or all float32.
+    w_post None: z = O; gate None: 1.
     norm(v) = v / sqrt(mean(v^2) + eps), row by row.  Written where given: H <- h (may
     be X or O itself), Y <- y, Q with S <- y in 8 bits (float8_e4m3fn with S
     (ceil(cols/128), rows), or int8 with S (rows)), H8 with SH and O8 with SO <- h and O

@@ -5,6 +5,7 @@
 // addresses of the library's functions and torch's functions for streams and devices.
 #include <Python.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include <cstdarg>
 #include <cstdint>
@@ -488,5 +489,13 @@ PyMODINIT_FUNC PyInit__tensors()
 {
     if (!stream_name && !(stream_name = PyUnicode_InternFromString("cuda_stream")))
         return nullptr;
-    return PyModule_Create(&module);
+    PyObject *m = PyModule_Create(&module);
+    // native.py compares it with what runs: the tensors' layout is that of this torch
+#define TEXT(x) #x
+#define VERSION(major, minor) TEXT(major) "." TEXT(minor) " " TORCH_VERSION
+    if (m && PyModule_AddStringConstant(m, "built_for", VERSION(PY_MAJOR_VERSION, PY_MINOR_VERSION)) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
 }

@@ -6,6 +6,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 
 from .sgemm import SGEMM_OK, SgemmError, load, sgemm_f32_status_string
 
@@ -32,6 +33,11 @@ def _bind():
             raise RuntimeError(f"_tensors.so does not load ({e}): it is built for one Python and one torch; build it again "
                                "(python -m fp32_gemm_08_amd.build)") from e
         raise RuntimeError("_tensors.so is missing: build it (python -m fp32_gemm_08_amd.build)") from e
+    python, version = getattr(_tensors, "built_for", "? ?").split()
+    if python != f"{sys.version_info.major}.{sys.version_info.minor}" or not torch.__version__.startswith(version):
+        raise RuntimeError(f"_tensors.so is built for Python {python} and torch {version}, not for "
+                           f"{sys.version_info.major}.{sys.version_info.minor} and {torch.__version__}: build it again "
+                           "(python -m fp32_gemm_08_amd.build)")
     lib = load()
     _tensors.bind(tuple(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in CALLS),
                   torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, torch._C._cuda_setDevice)
